@@ -1,60 +1,757 @@
 // Attention of one new token per sequence over the paged 4-bit cache.  C ABI:
 // include/maple_attn.h.
+//
+// Mathematics.  For a group of 8 query heads that share a key/value head, the
+// scores of 16 cached tokens are S^T = K Q^T (rows = tokens, columns = heads)
+// and the output O^T += V^T P^T, both on m16n8k16 matrix instructions with the
+// cached side as the 16-row operand, so that 8 heads fill an instruction.  A
+// running maximum and sum per head make one pass over the cache enough.
+//
+// The 4-bit codes c go into the matrix instructions as fp16 integers, exactly:
+// (w & 0x000f000f) | 0x64006400 is the pair (1024 + c, 1024 + c'), and with
+// 0x00f000f0 it is 1024 + 16 c, whose partner q is divided by 16.  The constant
+// part, 1024 sum q (64 sum q), enters as the accumulator's start value.  With
+// scale s and minimum m of a token's group of 32 channels,
+//   q.k = sum_groups s_g (q_g . c_g) + m_g sum(q_g)
+// in 32 bits: the scores carry no rounding of the dequantised keys.  q is
+// brought to [1, 2) by a power of two per head first (exact), so that fp16
+// holds it whatever its size.  Values are dequantised to fp16 (one rounding,
+// 2^-12) and p, scaled by 2^8, is rounded to fp16 (bf16 outputs) or split in
+// two fp16 terms (fp16 outputs, where one rounding of p would show).
+//
+// Work split.  All (sequence, key/value head) segments are laid end to end in
+// units of 64 tokens and every CTA takes an equal share of the line, so that a
+// batch of very different lengths keeps all SMs busy to the end.  A segment
+// that lies in one CTA is finished there; a cut one leaves partial results (at
+// most two per CTA) that combine_kernel joins in the order of the CTAs, so the
+// result is the same every time.  Short bounds (a window) take one CTA per
+// segment and no second kernel.
+//
+// Within a CTA each warp streams its own tiles of 64 tokens with bulk copies,
+// one tile ahead (one issuing thread per SM would not reach the memory's rate).
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "../../include/maple_attn.h"
 #include "kv_cache.cuh"
+#include "ptx.cuh"
 
 using namespace maple;
 
 namespace {
 
+constexpr int kWarps = 8, kStages = 2, kTile = 64;
+constexpr int kCtas = 148;          // CTAs that share the line of all segments (one per SM)
+constexpr int kSegCost = 4;         // tiles that a segment's own start and end are worth (a rough measure: about 2 us)
+constexpr int kWholeTiles = 16;     // segments of at most so many tiles: one CTA each, no combine
+
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
-// One warp per sequence and query head, one cached token at a time.
-template <typename T, int D>
-__global__ void __launch_bounds__(32) cached_rows_kernel(const maple_attn_cached_args a)
+struct CachedK {
+    maple_attn_cached_args a;
+    int NT, HB, cols;               // head tiles of 8, head blocks per key/value head, kv_heads * HB
+    int whole;
+    int64_t *prefix;                // [B] weight of the line before each sequence
+    float *part_ml;                 // [2 kCtas][8 NT][2]
+    float *part_o;                  // [2 kCtas][8 NT][D]
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t lo_codes(uint32_t w) { return (w & 0x000f000fu) | 0x64006400u; }
+__device__ __forceinline__ uint32_t hi_codes(uint32_t w) { return (w & 0x00f000f0u) | 0x64006400u; }
+__device__ __forceinline__ __half2 as_h2(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+
+// A sequence's tokens that its query sees, in tiles of 64
+struct Span {
+    int len, start, c0, n;
+    __device__ __forceinline__ void load(const maple_attn_cached_args &a, int b)
+    {
+        const int64_t cap = (int64_t)a.max_pages * a.page_size;
+        int64_t l = __ldg(a.lens + b);
+        if (l > cap) l = cap;
+        len = (int)l;
+        start = a.window && len > a.window ? len - a.window : 0;
+        c0 = start / kTile;
+        n = len > 0 ? (len + kTile - 1) / kTile - c0 : 0;
+    }
+};
+
+// How many CTAs share a line of `total` weight: each has a tile per warp at least
+__device__ __forceinline__ int sharers(int64_t total) { return (int)min((int64_t)kCtas, (total + kWarps - 1) / kWarps); }
+
+template <int D>
+struct CachedSmem {
+    static constexpr int kTileBytes = kTile * KvPage<D>::kRowBytes;
+    static constexpr int kBars = kWarps * kStages * kTileBytes;
+    static constexpr int kMax = kBars + 256;                               // [kWarps][16] maxima
+    static constexpr int kSum = kMax + kWarps * 16 * 4;                    // [kWarps / 2][16] sums
+    static constexpr int kAcc = kSum + kWarps / 2 * 16 * 4;                // [kWarps / 2][NT][D / 16][32 lanes] float4
+    static constexpr int total(int NT) { return kAcc + kWarps / 2 * NT * (D / 16) * 512; }
+};
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
 {
     using P = KvPage<D>;
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x, h = blockIdx.x, b = blockIdx.y, kvh = h / (a.heads / a.kv_heads), n = a.page_size;
-    int64_t len = a.lens[b];
-    if (len > (int64_t)a.max_pages * n) {
-        len = (int64_t)a.max_pages * n;
-        if (lane == 0) set_flag(a.flags, MAPLE_DEVFLAG_BAD_INDEX);
+    using L = CachedSmem<D>;
+    constexpr int G = D / 32, MT = D / 16;     // groups of 32 channels, 16-channel tiles of V^T
+    constexpr bool kSplitP = sizeof(T) == 2 && !__is_same(T, __nv_bfloat16);
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t s_scan[kWarps + 1];
+    __shared__ int64_t s_first[2];
+    __shared__ uint32_t s_abort;
+    const maple_attn_cached_args &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int n = a.page_size, ln = 31 - __clz(n), ppt = kTile >> ln;   // tokens of a page, pages of a tile
+    const int page_bytes = P::bytes(n);
+    const uint32_t bar0 = smem_addr(smem + L::kBars) + warp * kStages * 8;
+    if (lane == 0) {
+        for (int s = 0; s < kStages; s++) mbar_init(bar0 + 8 * s, 1);
+        fence_barrier_init();
     }
-    float q[E], o[E], mx = -INFINITY, sum = 0.0f;
-    const T *qp = (const T *)a.q + b * a.q_stride + (int64_t)h * D + lane * E;
-    for (int e = 0; e < E; e++) {
-        q[e] = (float)qp[e] * a.scale;
-        o[e] = 0.0f;
-    }
-    for (int64_t j = a.window ? max(len - a.window, (int64_t)0) : 0; j < len; j++) {
-        const int64_t pg = a.block_table[b * a.table_stride + j / n];
-        if (pg < 0 || pg >= a.num_pages) {
-            if (lane == 0) set_flag(a.flags, MAPLE_DEVFLAG_BAD_INDEX);
-            continue;
+    if (threadIdx.x == 0) s_abort = 0;
+    volatile uint32_t *abort = &s_abort;
+
+    // ---- this CTA's share of the line [R0, R1) and the segment that R0 falls into
+    int64_t R0, R1, W;
+    int b, col;
+    if (p.whole) {
+        b = blockIdx.x / p.cols;
+        col = blockIdx.x - b * p.cols;
+        W = R0 = 0;
+        R1 = 1ll << 40;
+        __syncthreads();
+    } else {
+        const int per = (a.B + blockDim.x - 1) / blockDim.x, lo = min((int)threadIdx.x * per, a.B), hi = min(lo + per, a.B);
+        int64_t mine = 0;
+        for (int i = lo; i < hi; i++) {
+            Span s;
+            s.load(a, i);
+            mine += (int64_t)p.cols * (s.n + kSegCost);
         }
-        const int p = (int)(j % n);
-        const uint8_t *base = a.pages + (pg * a.kv_heads + kvh) * P::bytes(n);
-        float s = 0.0f, v[E];
-        for (int e = 0; e < E; e++) {
-            const int c = lane * E + e, w = c / 8, sh = 4 * (c % 8), g = c / 32;
-            const uint32_t kw = *(const uint32_t *)(base + P::k_word(p, w)), vw = *(const uint32_t *)(base + P::v_word(n, p, w));
-            const float2 kp = __half22float2(*(const __half2 *)(base + P::k_pair(n, p, g)));
-            s = fmaf(q[e], fmaf(kp.x, (float)((kw >> sh) & 15u), kp.y), s);
-            v[e] = fmaf(__half2float(*(const __half *)(base + P::v_scale(n, p, g))), (float)((vw >> sh) & 15u),
-                        __half2float(*(const __half *)(base + P::v_min(n, p, g))));
+        int64_t inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(FULL, inc, o);
+            if (lane >= o) inc += v;
         }
-        s = warp_tree_sum(s);
-        const float m2 = fmaxf(mx, s), c = mx == -INFINITY ? 0.0f : expf(mx - m2), pr = expf(s - m2);
-        sum = fmaf(sum, c, pr);
-        for (int e = 0; e < E; e++) o[e] = fmaf(o[e], c, pr * v[e]);
-        mx = m2;
+        if (lane == 31) s_scan[warp] = inc;
+        __syncthreads();
+        int64_t before = inc - mine, total = 0;
+        for (int w = 0; w < kWarps; w++) {
+            if (w < warp) before += s_scan[w];
+            total += s_scan[w];
+        }
+        const int ns = sharers(total);
+        if ((int)blockIdx.x >= ns) return;
+        R0 = total * blockIdx.x / ns;
+        R1 = total * (blockIdx.x + 1) / ns;
+        int64_t at = before;
+        for (int i = lo; i < hi; i++) {
+            Span s;
+            s.load(a, i);
+            const int64_t w = (int64_t)p.cols * (s.n + kSegCost);
+            if (blockIdx.x == 0) p.prefix[i] = at;
+            if (R0 >= at && R0 < at + w) {
+                s_first[0] = i;
+                s_first[1] = at;
+            }
+            at += w;
+        }
+        __syncthreads();
+        b = (int)s_first[0];
+        Span s;
+        s.load(a, b);
+        col = (int)((R0 - s_first[1]) / (s.n + kSegCost));
+        W = s_first[1] + (int64_t)col * (s.n + kSegCost);
     }
-    T *op = (T *)a.out + ((int64_t)b * a.heads + h) * D + lane * E;
-    for (int e = 0; e < E; e++) op[e] = (T)(mx == -INFINITY ? 0.0f : o[e] / sum);
+    const int b_end = p.whole ? b + 1 : a.B;
+
+    // ---- the warp's tiles, one after another over all segments of the share
+    struct Walk {
+        int b, col;
+        int64_t W;
+        Span s;
+        int tile, end;      // next tile of this warp and the end of the share in the current segment
+        int first, last;    // the share's tiles of this segment, counted from the segment's first
+    };
+    auto enter = [&](Walk &w) {
+        w.first = (int)max(R0 - w.W - kSegCost, (int64_t)0);
+        w.last = (int)min(max(R1 - w.W - kSegCost, (int64_t)0), (int64_t)w.s.n);
+        w.tile = w.first + warp;
+        w.end = w.last;
+    };
+    auto next_segment = [&](Walk &w) -> bool {
+        w.W += w.s.n + kSegCost;
+        if (++w.col == p.cols || p.whole) {
+            w.col = 0;
+            if (++w.b >= b_end) return false;
+            w.s.load(a, w.b);
+        }
+        if (w.W >= R1) return false;
+        enter(w);
+        return true;
+    };
+
+    Walk pf;
+    pf.b = b;
+    pf.col = col;
+    pf.W = W;
+    pf.s.load(a, b);
+    enter(pf);
+    Walk cur = pf;
+    bool have = true;
+    int page = -1;              // lane i: page of the candidate's i-th page, loaded one step ahead of its copy
+    bool wanted = false;
+    auto settle = [&]() {       // to the next tile of this warp, and its pages' numbers on their way
+        while (have && pf.tile >= pf.end) have = next_segment(pf);
+        page = -1;
+        wanted = false;
+        if (have && lane < ppt) {
+            const int64_t j0 = (int64_t)(pf.s.c0 + pf.tile) * kTile + lane * n;
+            wanted = j0 < pf.s.len && j0 + n > pf.s.start;
+            if (wanted) page = __ldg(a.block_table + (int64_t)pf.b * a.table_stride + (j0 >> ln));
+        }
+    };
+    uint32_t okmask[kStages];   // pages of a stage that hold tokens
+    auto issue = [&](int s) {
+        okmask[s] = 0;
+        if (have) {
+            const bool good = wanted && page >= 0 && page < a.num_pages;
+            if (wanted && !good) set_flag(a.flags, MAPLE_DEVFLAG_BAD_INDEX);
+            const uint32_t m = __ballot_sync(FULL, good);
+            okmask[s] = m;
+            const uint32_t bar = bar0 + 8 * s;
+            if (lane == 0) {
+                if (m) mbar_expect_tx(bar, __popc(m) * page_bytes);
+                else mbar_arrive(bar);
+            }
+            __syncwarp();
+            if (good)
+                bulk_g2s(smem_addr(smem + (warp * kStages + s) * L::kTileBytes + lane * page_bytes),
+                         a.pages + ((int64_t)page * a.kv_heads + pf.col / p.HB) * page_bytes, page_bytes, bar);
+            pf.tile += kWarps;
+            settle();
+        }
+    };
+    settle();
+    uint32_t issued = 0, used = 0;   // tiles of this warp
+#pragma unroll
+    for (int s = 0; s < kStages; s++) {
+        if (have) issued++;
+        issue(s);
+    }
+
+    const int heads_per = a.heads / a.kv_heads;
+    bool dead = false;
+    for (bool more = true; more;) {
+        const int kvh = cur.col / p.HB, h0 = (cur.col - kvh * p.HB) * 8 * NT;
+        const int nh = min(8 * NT, heads_per - h0);              // heads of this block
+        const int ntile = cur.last - cur.first;
+        const bool empty = cur.s.n == 0 && R0 <= cur.W;          // no tokens: the share that holds its start writes zeros
+        if (R0 <= cur.W && threadIdx.x == 0 && __ldg(a.lens + cur.b) > (int64_t)a.max_pages * n)
+            set_flag(a.flags, MAPLE_DEVFLAG_BAD_INDEX);
+        if (ntile > 0 || empty) {
+            // ---- queries: B fragments, their sums, and the softmax scale of this lane's two heads
+            uint32_t qf[NT][G][4];
+            float qs[NT][G][2], qb[NT][G][2], sc[NT][2];
+#pragma unroll
+            for (int j = 0; j < NT; j++) {
+                const int h = j * 8 + g;
+                uint4 raw[G];
+#pragma unroll
+                for (int i = 0; i < G; i++) raw[i] = make_uint4(0, 0, 0, 0);
+                if (h < nh && ntile > 0) {
+                    const T *src = (const T *)a.q + (int64_t)cur.b * a.q_stride + (int64_t)(kvh * heads_per + h0 + h) * D + 8 * t;
+#pragma unroll
+                    for (int i = 0; i < G; i++) raw[i] = __ldg(reinterpret_cast<const uint4 *>(src + 32 * i));
+                }
+                float amax = 0.0f;
+#pragma unroll
+                for (int i = 0; i < G; i++) {
+                    float x[8];
+                    unpack8<T>(raw[i], x);
+#pragma unroll
+                    for (int m = 0; m < 8; m++) amax = fmaxf(amax, fabsf(x[m]));
+                }
+                amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 2));
+                // 2^-e with amax * 2^-e in [1, 2) (as far as 2^-e and 2^e are normal); 1 for zero and what is not finite
+                int e = (int)(__float_as_uint(amax) >> 23) - 127;
+                if (e >= 127 || e < -120) e = e == 127 ? 126 : (amax == 0.0f || e == 128 ? 0 : -120);
+                const float down = __int_as_float((127 - e) << 23);
+                float mine_sc = a.scale * 1.4426950408889634f * __int_as_float((127 + e) << 23);
+#pragma unroll
+                for (int i = 0; i < G; i++) {
+                    float x[8];
+                    unpack8<T>(raw[i], x);
+#pragma unroll
+                    for (int m = 0; m < 8; m++) x[m] = x[m] * down * ((m & 1) ? 0.0625f : 1.0f);
+                    float sum = 0.0f, bias = 0.0f;
+#pragma unroll
+                    for (int m = 0; m < 4; m++) {
+                        const __half2 v = __floats2half2_rn(x[m], x[m + 4]);
+                        qf[j][i][m] = as_u32(v);
+                        const float2 f = __half22float2(v);
+                        bias += f.x + f.y;
+                        sum += (m & 1) ? 16.0f * (f.x + f.y) : f.x + f.y;
+                    }
+                    sum += __shfl_xor_sync(FULL, sum, 1);
+                    sum += __shfl_xor_sync(FULL, sum, 2);
+                    bias += __shfl_xor_sync(FULL, bias, 1);
+                    bias += __shfl_xor_sync(FULL, bias, 2);
+#pragma unroll
+                    for (int c = 0; c < 2; c++) {
+                        qs[j][i][c] = __shfl_sync(FULL, sum, (2 * t + c) * 4);
+                        qb[j][i][c] = -1024.0f * __shfl_sync(FULL, bias, (2 * t + c) * 4);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 2; c++) sc[j][c] = __shfl_sync(FULL, mine_sc, (2 * t + c) * 4);
+            }
+            float O[NT][MT][4], mx[NT][2], sum[NT][2];
+#pragma unroll
+            for (int j = 0; j < NT; j++) {
+#pragma unroll
+                for (int i = 0; i < MT; i++)
+#pragma unroll
+                    for (int c = 0; c < 4; c++) O[j][i][c] = 0.0f;
+                mx[j][0] = mx[j][1] = -INFINITY;
+                sum[j][0] = sum[j][1] = 0.0f;
+            }
+
+            // ---- this warp's tiles of the segment
+            for (int tile = cur.first + warp; tile < cur.last; tile += kWarps) {
+                const int s = used % kStages;
+                if (!dead && !mbar_wait(bar0 + 8 * s, (used / kStages) & 1, abort, a.flags, kDefaultWaitNs)) dead = true;
+                dead = __any_sync(FULL, dead);
+                const uint8_t *buf = smem + (warp * kStages + s) * L::kTileBytes;
+                uint32_t ok = 0;
+#pragma unroll
+                for (int q = 0; q < kStages; q++)
+                    if (q == s) ok = okmask[q];
+                const int j0 = (cur.s.c0 + tile) * kTile;
+                const bool edge = j0 < cur.s.start || j0 + kTile > cur.s.len || ok != (1u << ppt) - 1;
+                if (!dead) {
+                    float S[NT][4][4];
+#pragma unroll
+                    for (int kb = 0; kb < 4; kb++) {
+                        const int pg = (kb * 16) >> ln, r0 = kb * 16 - (pg << ln);
+                        const uint8_t *base = buf + pg * page_bytes;
+                        uint32_t w0[G], w1[G], pr0[G], pr1[G];
+                        if (G == 4) {
+                            *(uint4 *)w0 = *(const uint4 *)(base + (r0 + g) * (D / 2) + t * 16);
+                            *(uint4 *)w1 = *(const uint4 *)(base + (r0 + g + 8) * (D / 2) + t * 16);
+                            *(uint4 *)pr0 = *(const uint4 *)(base + P::k_pair(n, r0 + g, 0));
+                            *(uint4 *)pr1 = *(const uint4 *)(base + P::k_pair(n, r0 + g + 8, 0));
+                        } else {
+                            *(uint2 *)w0 = *(const uint2 *)(base + (r0 + g) * (D / 2) + t * 8);
+                            *(uint2 *)w1 = *(const uint2 *)(base + (r0 + g + 8) * (D / 2) + t * 8);
+                            *(uint2 *)pr0 = *(const uint2 *)(base + P::k_pair(n, r0 + g, 0));
+                            *(uint2 *)pr1 = *(const uint2 *)(base + P::k_pair(n, r0 + g + 8, 0));
+                        }
+#pragma unroll
+                        for (int j = 0; j < NT; j++) S[j][kb][0] = S[j][kb][1] = S[j][kb][2] = S[j][kb][3] = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < G; i++) {
+                            const uint32_t a0 = lo_codes(w0[i]), a1 = lo_codes(w1[i]), a2 = hi_codes(w0[i]), a3 = hi_codes(w1[i]);
+                            const uint32_t x0 = w0[i] >> 8, x1 = w1[i] >> 8;
+                            const uint32_t c0 = lo_codes(x0), c1 = lo_codes(x1), c2 = hi_codes(x0), c3 = hi_codes(x1);
+                            const float2 f0 = __half22float2(as_h2(pr0[i])), f1 = __half22float2(as_h2(pr1[i]));
+#pragma unroll
+                            for (int j = 0; j < NT; j++) {
+                                float c[4] = {qb[j][i][0], qb[j][i][1], qb[j][i][0], qb[j][i][1]};
+                                mma16(c, a0, a1, a2, a3, qf[j][i][0], qf[j][i][1]);
+                                mma16(c, c0, c1, c2, c3, qf[j][i][2], qf[j][i][3]);
+                                S[j][kb][0] = fmaf(f0.x, c[0], fmaf(f0.y, qs[j][i][0], S[j][kb][0]));
+                                S[j][kb][1] = fmaf(f0.x, c[1], fmaf(f0.y, qs[j][i][1], S[j][kb][1]));
+                                S[j][kb][2] = fmaf(f1.x, c[2], fmaf(f1.y, qs[j][i][0], S[j][kb][2]));
+                                S[j][kb][3] = fmaf(f1.x, c[3], fmaf(f1.y, qs[j][i][1], S[j][kb][3]));
+                            }
+                        }
+                        if (edge) {
+                            const bool okp = (ok >> pg) & 1;
+#pragma unroll
+                            for (int half = 0; half < 2; half++) {
+                                const int key = j0 + kb * 16 + g + 8 * half;
+                                if (!okp || key < cur.s.start || key >= cur.s.len) {
+#pragma unroll
+                                    for (int j = 0; j < NT; j++) S[j][kb][2 * half] = S[j][kb][2 * half + 1] = -INFINITY;
+                                }
+                            }
+                        }
+                    }
+                    // ---- running maximum, weights
+#pragma unroll
+                    for (int j = 0; j < NT; j++) {
+                        float mn[2];
+                        bool moved = false;
+#pragma unroll
+                        for (int c = 0; c < 2; c++) {
+                            // (a negative scale turns the order: the maximum is taken of the scaled scores)
+                            float m = -INFINITY;
+#pragma unroll
+                            for (int kb = 0; kb < 4; kb++) {
+#pragma unroll
+                                for (int half = 0; half < 2; half++) {
+                                    float &v = S[j][kb][2 * half + c];
+                                    v = v == -INFINITY && edge ? v : v * sc[j][c];
+                                    m = fmaxf(m, v);
+                                }
+                            }
+                            m = fmaxf(m, __shfl_xor_sync(FULL, m, 4));
+                            m = fmaxf(m, __shfl_xor_sync(FULL, m, 8));
+                            m = fmaxf(m, __shfl_xor_sync(FULL, m, 16));
+                            mn[c] = fmaxf(mx[j][c], m);
+                            moved = moved || mn[c] > mx[j][c];
+                        }
+                        if (__any_sync(FULL, moved)) {
+                            float f[2];
+#pragma unroll
+                            for (int c = 0; c < 2; c++) {
+                                f[c] = mx[j][c] == -INFINITY ? 0.0f : ex2(mx[j][c] - mn[c]);
+                                sum[j][c] *= f[c];
+                                mx[j][c] = mn[c];
+                            }
+#pragma unroll
+                            for (int i = 0; i < MT; i++) {
+                                O[j][i][0] *= f[0];
+                                O[j][i][1] *= f[1];
+                                O[j][i][2] *= f[0];
+                                O[j][i][3] *= f[1];
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < 2; c++) {
+                            const float off = mx[j][c] == -INFINITY ? 0.0f : 8.0f - mx[j][c];
+#pragma unroll
+                            for (int kb = 0; kb < 4; kb++)
+#pragma unroll
+                                for (int half = 0; half < 2; half++) {
+                                    float &v = S[j][kb][2 * half + c];
+                                    v = ex2(v + off);
+                                    sum[j][c] += v;
+                                }
+                        }
+                    }
+                    // ---- O^T += V^T P^T
+#pragma unroll
+                    for (int kb = 0; kb < 4; kb++) {
+                        const int pg = (kb * 16) >> ln, r0 = kb * 16 - (pg << ln);
+                        const uint8_t *base = buf + pg * page_bytes;
+                        const uint8_t *vb = base + n * (D / 2) + (r0 >> 4) * (8 * D) + lane * 16;
+                        const int gg = g * (D / 8) / 32;   // the group of this lane's channels
+                        // scales and minima of tokens (2t, 2t+1) and (2t+8, 2t+9)
+                        uint32_t s0 = *(const uint32_t *)(base + P::v_scale(n, r0 + 2 * t, gg));
+                        uint32_t s1 = *(const uint32_t *)(base + P::v_scale(n, r0 + 2 * t + 8, gg));
+                        uint32_t m0 = *(const uint32_t *)(base + P::v_min(n, r0 + 2 * t, gg));
+                        uint32_t m1 = *(const uint32_t *)(base + P::v_min(n, r0 + 2 * t + 8, gg));
+                        if (edge) {   // rows without a token may hold anything: their weight is 0, their value too
+                            const bool okp = (ok >> pg) & 1;
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                const int key = j0 + kb * 16 + 2 * t + (i & 1) + 8 * (i >> 1);
+                                if (!okp || key < cur.s.start || key >= cur.s.len) {
+                                    const uint32_t keep = (i & 1) ? 0x0000ffffu : 0xffff0000u;
+                                    if (i < 2) { s0 &= keep; m0 &= keep; }
+                                    else { s1 &= keep; m1 &= keep; }
+                                }
+                            }
+                        }
+                        uint32_t pb[NT][2], pl[NT][2];
+#pragma unroll
+                        for (int j = 0; j < NT; j++)
+#pragma unroll
+                            for (int half = 0; half < 2; half++) {
+                                const float v0 = S[j][kb][2 * half], v1 = S[j][kb][2 * half + 1];
+                                const __half2 hi = __floats2half2_rn(v0, v1);
+                                pb[j][half] = transpose8(as_u32(hi));
+                                if (kSplitP) {
+                                    const float2 f = __half22float2(hi);
+                                    pl[j][half] = transpose8(as_u32(__floats2half2_rn(v0 - f.x, v1 - f.y)));
+                                }
+                            }
+                        const __half2 k1024 = __float2half2_rn(-1024.0f), k64 = __float2half2_rn(-64.0f), k16 = __float2half2_rn(0.0625f);
+                        auto deq_lo = [&](uint32_t w, uint32_t s, uint32_t m) {
+                            return as_u32(__hfma2(__hadd2(as_h2(lo_codes(w)), k1024), as_h2(s), as_h2(m)));
+                        };
+                        auto deq_hi = [&](uint32_t w, uint32_t s, uint32_t m) {
+                            return as_u32(__hfma2(__hfma2(as_h2(hi_codes(w)), k16, k64), as_h2(s), as_h2(m)));
+                        };
+                        uint4 va = *(const uint4 *)vb, vc = va;
+                        if (D == 128) vc = *(const uint4 *)(vb + 512);
+                        // words of tokens 2t, 2t+1 (e, o) and 2t+8, 2t+9 (e8, o8)
+                        constexpr int NW = D / 64;
+                        const uint32_t e[2] = {va.x, va.y}, o[2] = {D == 128 ? va.z : va.y, va.w};
+                        const uint32_t e8[2] = {D == 128 ? vc.x : vc.z, vc.y}, o8[2] = {D == 128 ? vc.z : vc.w, vc.w};
+#pragma unroll
+                        for (int w = 0; w < NW; w++)
+#pragma unroll
+                            for (int q = 0; q < 2; q++) {   // channels 4q .. 4q+3 of the word
+                                uint32_t x = __byte_perm(e[w], o[w], q ? 0x7632 : 0x5410);
+                                uint32_t y = __byte_perm(e8[w], o8[w], q ? 0x7632 : 0x5410);
+#pragma unroll
+                                for (int z = 0; z < 2; z++) {
+                                    const uint32_t a0 = deq_lo(x, s0, m0), a1 = deq_hi(x, s0, m0);
+                                    const uint32_t a2 = deq_lo(y, s1, m1), a3 = deq_hi(y, s1, m1);
+#pragma unroll
+                                    for (int j = 0; j < NT; j++) {
+                                        mma16(O[j][w * 4 + q * 2 + z], a0, a1, a2, a3, pb[j][0], pb[j][1]);
+                                        if (kSplitP) mma16(O[j][w * 4 + q * 2 + z], a0, a1, a2, a3, pl[j][0], pl[j][1]);
+                                    }
+                                    x >>= 8;
+                                    y >>= 8;
+                                }
+                            }
+                    }
+                }
+                __syncwarp();
+                used++;
+                if (have) issued++;
+#pragma unroll
+                for (int q = 0; q < kStages; q++)
+                    if (q == s) issue(q);
+            }
+
+            // ---- join the warps: common maximum, then sums in a fixed tree
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    sum[j][c] += __shfl_xor_sync(FULL, sum[j][c], 4);
+                    sum[j][c] += __shfl_xor_sync(FULL, sum[j][c], 8);
+                    sum[j][c] += __shfl_xor_sync(FULL, sum[j][c], 16);
+                }
+            float *s_max = (float *)(smem + L::kMax), *s_sum = (float *)(smem + L::kSum);
+            float4 *s_acc = (float4 *)(smem + L::kAcc);
+            if (g == 0)
+#pragma unroll
+                for (int j = 0; j < NT; j++)
+#pragma unroll
+                    for (int c = 0; c < 2; c++) s_max[warp * 16 + j * 8 + 2 * t + c] = mx[j][c];
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < NT; j++) {
+                float f[2];
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    float m = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < kWarps; w++) m = fmaxf(m, s_max[w * 16 + j * 8 + 2 * t + c]);
+                    f[c] = mx[j][c] == -INFINITY ? 0.0f : ex2(mx[j][c] - m);
+                    mx[j][c] = m;
+                    sum[j][c] *= f[c];
+                }
+#pragma unroll
+                for (int i = 0; i < MT; i++) {
+                    O[j][i][0] *= f[0];
+                    O[j][i][1] *= f[1];
+                    O[j][i][2] *= f[0];
+                    O[j][i][3] *= f[1];
+                }
+            }
+            const int busy = min(kWarps, ntile);    // (warps beyond the tiles hold zeros)
+            for (int m = busy; m > 1;) {
+                const int half = (m + 1) / 2;
+                if (warp >= half && warp < m) {
+#pragma unroll
+                    for (int j = 0; j < NT; j++) {
+#pragma unroll
+                        for (int i = 0; i < MT; i++)
+                            s_acc[(((warp - half) * NT + j) * MT + i) * 32 + lane] =
+                                make_float4(O[j][i][0], O[j][i][1], O[j][i][2], O[j][i][3]);
+                        if (g == 0) {
+                            s_sum[(warp - half) * 16 + j * 8 + 2 * t] = sum[j][0];
+                            s_sum[(warp - half) * 16 + j * 8 + 2 * t + 1] = sum[j][1];
+                        }
+                    }
+                }
+                __syncthreads();
+                if (warp < m - half) {
+#pragma unroll
+                    for (int j = 0; j < NT; j++) {
+#pragma unroll
+                        for (int i = 0; i < MT; i++) {
+                            const float4 v = s_acc[((warp * NT + j) * MT + i) * 32 + lane];
+                            O[j][i][0] += v.x;
+                            O[j][i][1] += v.y;
+                            O[j][i][2] += v.z;
+                            O[j][i][3] += v.w;
+                        }
+                        sum[j][0] += s_sum[warp * 16 + j * 8 + 2 * t];
+                        sum[j][1] += s_sum[warp * 16 + j * 8 + 2 * t + 1];
+                    }
+                }
+                __syncthreads();
+                m = half;
+            }
+            // ---- warp 0 holds the segment's (or the share's) result
+            if (warp == 0) {
+                const bool whole_seg = cur.first == 0 && cur.last == cur.s.n;
+                const int slot = 2 * blockIdx.x + (R0 >= cur.W ? 0 : 1);
+                constexpr int CH = D / 8;          // channels of this lane, CH*g ..
+#pragma unroll
+                for (int j = 0; j < NT; j++)
+#pragma unroll
+                    for (int c = 0; c < 2; c++) {
+                        const int h = j * 8 + 2 * t + c;
+                        if (h >= nh) continue;
+                        float x[CH];
+#pragma unroll
+                        for (int i = 0; i < MT; i++) {
+                            x[2 * i] = O[j][i][c];
+                            x[2 * i + 1] = O[j][i][c + 2];
+                        }
+                        if (whole_seg) {
+                            const float inv = sum[j][c] > 0.0f || sum[j][c] != sum[j][c] ? __fdiv_rn(1.0f, sum[j][c]) : 0.0f;
+                            T *dst = (T *)a.out + ((int64_t)cur.b * a.heads + kvh * heads_per + h0 + h) * D + CH * g;
+#pragma unroll
+                            for (int i = 0; i < CH; i += 8) {
+                                float y[8];
+#pragma unroll
+                                for (int m = 0; m < 8; m++) y[m] = x[i + m] * inv;
+                                *reinterpret_cast<uint4 *>(dst + i) = pack8<T>(y);
+                            }
+                        } else {
+                            float *dst = p.part_o + ((int64_t)slot * 8 * NT + h) * D + CH * g;
+#pragma unroll
+                            for (int i = 0; i < CH; i += 4)
+                                *reinterpret_cast<float4 *>(dst + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                            if (g == 0) {
+                                p.part_ml[((int64_t)slot * 8 * NT + h) * 2] = mx[j][c];
+                                p.part_ml[((int64_t)slot * 8 * NT + h) * 2 + 1] = sum[j][c];
+                            }
+                        }
+                    }
+            }
+        }
+        more = next_segment(cur);
+    }
+    for (; used < issued; used++)   // copies still in flight (only after a failed wait)
+        mbar_wait(bar0 + 8 * (used % kStages), (used / kStages) & 1, abort, a.flags, kDefaultWaitNs);
+    asm volatile("griddepcontrol.launch_dependents;");
+}
+
+// Joins the partial results of segments that several CTAs share; one CTA per
+// (sequence, column), heads x D/4 threads, partial results in the CTAs' order.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(256) combine_kernel(const CachedK p)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const maple_attn_cached_args &a = p.a;
+    const int b = blockIdx.x / p.cols, col = blockIdx.x - b * p.cols;
+    Span s, e;
+    s.load(a, b);
+    e.load(a, a.B - 1);
+    if (s.n == 0) return;
+    const int64_t total = p.prefix[a.B - 1] + (int64_t)p.cols * (e.n + kSegCost);
+    const int ns = sharers(total);
+    const int64_t W = p.prefix[b] + (int64_t)col * (s.n + kSegCost);
+    // the share that holds position x of the line: the largest i with total * i / ns <= x
+    auto share = [&](int64_t x) { return (int)(((x + 1) * ns - 1) / total); };
+    const int i0 = share(W + kSegCost), i1 = share(W + kSegCost + s.n - 1);
+    if (i0 == i1) return;
+    const int heads_per = a.heads / a.kv_heads, kvh = col / p.HB, h0 = (col - kvh * p.HB) * 8 * NT;
+    const int nh = min(8 * NT, heads_per - h0);
+    auto slot = [&](int i) { return 2 * i + (total * i / ns >= W ? 0 : 1); };
+    for (int x = threadIdx.x; x < nh * (D / 4); x += blockDim.x) {
+        const int h = x / (D / 4), c = x - h * (D / 4);
+        float m = -INFINITY;
+        for (int i = i0; i <= i1; i++) m = fmaxf(m, p.part_ml[((int64_t)slot(i) * 8 * NT + h) * 2]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.0f;
+#pragma unroll 4
+        for (int i = i0; i <= i1; i++) {
+            const int64_t at = (int64_t)slot(i) * 8 * NT + h;
+            const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + at * 2);
+            const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
+            const float4 v = *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * c);
+            l = fmaf(ml.y, f, l);
+            acc.x = fmaf(v.x, f, acc.x);
+            acc.y = fmaf(v.y, f, acc.y);
+            acc.z = fmaf(v.z, f, acc.z);
+            acc.w = fmaf(v.w, f, acc.w);
+        }
+        const float inv = l > 0.0f || l != l ? __fdiv_rn(1.0f, l) : 0.0f;
+        uint2 o = make_uint2(Elem<T>::pack(acc.x * inv, acc.y * inv), Elem<T>::pack(acc.z * inv, acc.w * inv));
+        *reinterpret_cast<uint2 *>((T *)a.out + ((int64_t)b * a.heads + kvh * heads_per + h0 + h) * D + 4 * c) = o;
+    }
+}
+
+// the plan that the workspace and the launch share
+struct Plan {
+    int NT, HB, cols, whole;
+    int64_t prefix_bytes, ml_bytes, o_bytes;
+};
+Plan make_plan(int32_t B, int32_t max_pages, int32_t heads, int32_t kv_heads, int32_t D, int32_t page_size, int32_t window)
+{
+    Plan pl;
+    const int G = heads / kv_heads;
+    pl.NT = G <= 8 ? 1 : 2;
+    pl.HB = (G + 8 * pl.NT - 1) / (8 * pl.NT);
+    pl.cols = kv_heads * pl.HB;
+    int64_t tokens = (int64_t)max_pages * page_size;
+    if (window && tokens > (int64_t)window + kTile - 1) tokens = (int64_t)window + kTile - 1;
+    pl.whole = (tokens + kTile - 1) / kTile <= kWholeTiles;
+    pl.prefix_bytes = pl.whole ? 0 : ((int64_t)B * 8 + 255) / 256 * 256;
+    pl.ml_bytes = pl.whole ? 0 : (2ll * kCtas * 8 * pl.NT * 8 + 255) / 256 * 256;
+    pl.o_bytes = pl.whole ? 0 : 2ll * kCtas * 8 * pl.NT * D * 4;
+    return pl;
+}
+
+template <typename T, int D, int NT>
+int launch(const CachedK &k, cudaStream_t st)
+{
+    const int smem = CachedSmem<D>::total(NT);
+    if (cudaFuncSetAttribute(cached_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        cudaGetLastError();
+        return MAPLE_ERR_CUDA;
+    }
+    const int64_t segments = (int64_t)k.a.B * k.cols;
+    cached_kernel<T, D, NT><<<(unsigned)(k.whole ? segments : kCtas), kWarps * 32, smem, st>>>(k);
+    if (!k.whole) {
+        cudaLaunchConfig_t lc;
+        memset(&lc, 0, sizeof lc);
+        lc.gridDim = dim3((unsigned)segments);
+        lc.blockDim = dim3(256);
+        lc.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        lc.attrs = attr;
+        lc.numAttrs = 1;
+        if (cudaLaunchKernelEx(&lc, combine_kernel<T, D, NT>, k) != cudaSuccess) {
+            cudaGetLastError();
+            return MAPLE_ERR_CUDA;
+        }
+    }
+    return cudaGetLastError() == cudaSuccess ? MAPLE_OK : MAPLE_ERR_CUDA;
+}
+
+template <typename T>
+int launch_type(const CachedK &k, cudaStream_t st)
+{
+    if (k.a.head_dim == 128) return k.NT == 1 ? launch<T, 128, 1>(k, st) : launch<T, 128, 2>(k, st);
+    return k.NT == 1 ? launch<T, 64, 1>(k, st) : launch<T, 64, 2>(k, st);
 }
 
 }  // namespace
@@ -64,8 +761,9 @@ extern "C" int64_t maple_attn_cached_workspace(int32_t B, int32_t max_pages, int
 {
     if (maple_attn_page_bytes(head_dim, page_size) < 0 || heads < 1 || kv_heads < 1 || heads > 1024 || heads % kv_heads)
         return MAPLE_ERR_UNSUPPORTED_SHAPE;
-    if (B < 0 || B > 65535 || max_pages < 0 || window < 0) return MAPLE_ERR_INVALID_ARG;
-    return 0;
+    if (B < 0 || B > 65535 || max_pages < 0 || max_pages > (1 << 30) / page_size || window < 0) return MAPLE_ERR_INVALID_ARG;
+    const Plan pl = make_plan(B, max_pages, heads, kv_heads, head_dim, page_size, window);
+    return pl.prefix_bytes + pl.ml_bytes + pl.o_bytes;
 }
 
 extern "C" int maple_attn_cached(const maple_attn_cached_args *args, maple_stream_t stream)
@@ -84,14 +782,15 @@ extern "C" int maple_attn_cached(const maple_attn_cached_args *args, maple_strea
     for (const void *p : {a.q, (const void *)a.out, (const void *)a.pages, (const void *)a.workspace})
         if (!aligned16(p)) return MAPLE_ERR_INVALID_ARG;
     if (((uintptr_t)a.block_table & 3u) || ((uintptr_t)a.lens & 3u) || a.q_stride % 8) return MAPLE_ERR_INVALID_ARG;
-    cudaStream_t st = (cudaStream_t)stream;
-    const dim3 grid(a.heads, a.B);
-    if (a.dtype == MAPLE_BF16) {
-        if (a.head_dim == 128) cached_rows_kernel<__nv_bfloat16, 128><<<grid, 32, 0, st>>>(a);
-        else cached_rows_kernel<__nv_bfloat16, 64><<<grid, 32, 0, st>>>(a);
-    } else {
-        if (a.head_dim == 128) cached_rows_kernel<__half, 128><<<grid, 32, 0, st>>>(a);
-        else cached_rows_kernel<__half, 64><<<grid, 32, 0, st>>>(a);
-    }
-    return cudaGetLastError() == cudaSuccess ? MAPLE_OK : MAPLE_ERR_CUDA;
+    const Plan pl = make_plan(a.B, a.max_pages, a.heads, a.kv_heads, a.head_dim, a.page_size, a.window);
+    CachedK k;
+    k.a = a;
+    k.NT = pl.NT;
+    k.HB = pl.HB;
+    k.cols = pl.cols;
+    k.whole = pl.whole;
+    k.prefix = (int64_t *)a.workspace;
+    k.part_ml = (float *)((char *)a.workspace + pl.prefix_bytes);
+    k.part_o = (float *)((char *)a.workspace + pl.prefix_bytes + pl.ml_bytes);
+    return a.dtype == MAPLE_BF16 ? launch_type<__nv_bfloat16>(k, (cudaStream_t)stream) : launch_type<__half>(k, (cudaStream_t)stream);
 }
