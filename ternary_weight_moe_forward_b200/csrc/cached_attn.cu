@@ -16,7 +16,7 @@
 // in 32 bits: the scores carry no rounding of the dequantised keys.  q is
 // brought to [1, 2) by a power of two per head first (exact), so that fp16
 // holds it whatever its size.  Values are dequantised to fp16 (one rounding,
-// 2^-12) and p, scaled by 2^8, is rounded to fp16 (bf16 outputs) or split in
+// 2^-12) and p, scaled by 2^4, is rounded to fp16 (bf16 outputs) or split in
 // two fp16 terms (fp16 outputs, where one rounding of p would show).
 //
 // Work split.  All (sequence, key/value head) segments are laid end to end in
@@ -27,8 +27,9 @@
 // result is the same every time.  Short bounds (a window) take one CTA per
 // segment and no second kernel.
 //
-// Within a CTA each warp streams its own tiles of 64 tokens with bulk copies,
-// one tile ahead (one issuing thread per SM would not reach the memory's rate).
+// Within a CTA eight rings of tiles of 64 tokens are filled by a warp each with
+// bulk copies, one tile ahead (one issuing thread per SM would not reach the
+// memory's rate).
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -41,9 +42,9 @@ using namespace maple;
 
 namespace {
 
-constexpr int kWarps = 8, kStages = 2, kTile = 64;
+constexpr int kStages = 2, kTile = 64;   // tiles of a ring, tokens of a tile
 constexpr int kCtas = 148;          // CTAs that share the line of all segments (one per SM)
-constexpr int kSegCost = 4;         // tiles that a segment's own start and end are worth (a rough measure: about 2 us)
+constexpr int kSegCost = 12;        // tiles that a segment's own start and end are worth (a rough measure: about 2 us)
 constexpr int kWholeTiles = 16;     // segments of at most so many tiles: one CTA each, no combine
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -65,18 +66,34 @@ __device__ __forceinline__ float ex2(float x)
 }
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the same with every row of the accumulator starting at (c0, c1)
+__device__ __forceinline__ void mma16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                           uint32_t b1, float c0, float c1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t v)
 {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-__device__ __forceinline__ uint32_t lo_codes(uint32_t w) { return (w & 0x000f000fu) | 0x64006400u; }
-__device__ __forceinline__ uint32_t hi_codes(uint32_t w) { return (w & 0x00f000f0u) | 0x64006400u; }
+// (w & mask) | 0x64006400 in one instruction (written as two operators it became two)
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t codes(uint32_t w)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(MASK), "r"(0x64006400u));
+    return r;
+}
+__device__ __forceinline__ uint32_t lo_codes(uint32_t w) { return codes<0x000f000fu>(w); }
+__device__ __forceinline__ uint32_t hi_codes(uint32_t w) { return codes<0x00f000f0u>(w); }
 __device__ __forceinline__ __half2 as_h2(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 
@@ -95,24 +112,30 @@ struct Span {
     }
 };
 
-// How many CTAs share a line of `total` weight: each has a tile per warp at least
-__device__ __forceinline__ int sharers(int64_t total) { return (int)min((int64_t)kCtas, (total + kWarps - 1) / kWarps); }
+// How many CTAs share a line of `total` weight: each has 8 tiles at least
+__device__ __forceinline__ int sharers(int64_t total) { return (int)min((int64_t)kCtas, (total + 7) / 8); }
 
-template <int D>
+// PW warps share a tile (each takes 64 / PW of its tokens): two where the
+// accumulators of 8 heads leave registers for 16 warps, else one.
+template <int D, int NT>
 struct CachedSmem {
+    static constexpr int kRings = NT == 1 ? 10 : 8, PW = 1, kWarps = kRings * PW, kHalf = (kWarps + 1) / 2;
     static constexpr int kTileBytes = kTile * KvPage<D>::kRowBytes;
-    static constexpr int kBars = kWarps * kStages * kTileBytes;
-    static constexpr int kMax = kBars + 256;                               // [kWarps][16] maxima
-    static constexpr int kSum = kMax + kWarps * 16 * 4;                    // [kWarps / 2][16] sums
-    static constexpr int kAcc = kSum + kWarps / 2 * 16 * 4;                // [kWarps / 2][NT][D / 16][32 lanes] float4
-    static constexpr int total(int NT) { return kAcc + kWarps / 2 * NT * (D / 16) * 512; }
+    static constexpr int kBars = kRings * kStages * kTileBytes;
+    static constexpr int kOk = kBars + kRings * kStages * 8;               // pages of each ring's tiles that hold tokens
+    static constexpr int kMax = kOk + (kRings * kStages * 4 + 15) / 16 * 16;                // [kWarps][16] maxima
+    static constexpr int kSum = kMax + kWarps * 16 * 4;                    // [kHalf][16] sums
+    static constexpr int kAcc = kSum + (kHalf * 16 * 4 + 15) / 16 * 16;    // [kHalf][NT][D / 16][32 lanes] float4
+    static constexpr int kTotal = kAcc + kHalf * NT * (D / 16) * 512;
+    static_assert(kAcc % 16 == 0, "the accumulators are moved as float4");
 };
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
+template <typename T, int D, int NT, int N>
+__global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kernel(const CachedK p)
 {
     using P = KvPage<D>;
-    using L = CachedSmem<D>;
+    using L = CachedSmem<D, NT>;
+    constexpr int kRings = L::kRings, PW = L::PW, kWarps = L::kWarps, KB = 4 / PW;   // blocks of 16 tokens of a warp in a tile
     constexpr int G = D / 32, MT = D / 16;     // groups of 32 channels, 16-channel tiles of V^T
     constexpr bool kSplitP = sizeof(T) == 2 && !__is_same(T, __nv_bfloat16);
     extern __shared__ __align__(128) uint8_t smem[];
@@ -121,10 +144,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
     __shared__ uint32_t s_abort;
     const maple_attn_cached_args &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int n = a.page_size, ln = 31 - __clz(n), ppt = kTile >> ln;   // tokens of a page, pages of a tile
-    const int page_bytes = P::bytes(n);
-    const uint32_t bar0 = smem_addr(smem + L::kBars) + warp * kStages * 8;
-    if (lane == 0) {
+    constexpr int n = N, ppt = kTile / N;             // tokens of a page, pages of a tile
+    constexpr int page_bytes = P::bytes(N);
+    const int ring = warp / PW, sub = warp % PW;      // this warp's ring and its part of a tile
+    const bool loader = sub == 0;                     // the warp that copies the ring's tiles
+    const uint32_t bar0 = smem_addr(smem + L::kBars) + ring * kStages * 8;
+    volatile uint32_t *okmask = (volatile uint32_t *)(smem + L::kOk) + ring * kStages;
+    auto ring_sync = [&]() {   // the warps of a ring (the barriers' ids are 1 .. 8)
+        if (PW > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + ring), "r"(32 * PW) : "memory");
+        else __syncwarp();
+    };
+    if (loader && lane == 0) {
         for (int s = 0; s < kStages; s++) mbar_init(bar0 + 8 * s, 1);
         fence_barrier_init();
     }
@@ -186,18 +216,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
     }
     const int b_end = p.whole ? b + 1 : a.B;
 
-    // ---- the warp's tiles, one after another over all segments of the share
+    // ---- the ring's tiles, one after another over all segments of the share
     struct Walk {
         int b, col;
         int64_t W;
         Span s;
-        int tile, end;      // next tile of this warp and the end of the share in the current segment
+        int tile, end;      // next tile of this ring and the end of the share in the current segment
         int first, last;    // the share's tiles of this segment, counted from the segment's first
     };
     auto enter = [&](Walk &w) {
         w.first = (int)max(R0 - w.W - kSegCost, (int64_t)0);
         w.last = (int)min(max(R1 - w.W - kSegCost, (int64_t)0), (int64_t)w.s.n);
-        w.tile = w.first + warp;
+        w.tile = w.first + ring;
         w.end = w.last;
     };
     auto next_segment = [&](Walk &w) -> bool {
@@ -222,24 +252,22 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
     bool have = true;
     int page = -1;              // lane i: page of the candidate's i-th page, loaded one step ahead of its copy
     bool wanted = false;
-    auto settle = [&]() {       // to the next tile of this warp, and its pages' numbers on their way
+    auto settle = [&]() {       // to the next tile of this ring, and its pages' numbers on their way
         while (have && pf.tile >= pf.end) have = next_segment(pf);
         page = -1;
         wanted = false;
         if (have && lane < ppt) {
-            const int64_t j0 = (int64_t)(pf.s.c0 + pf.tile) * kTile + lane * n;
+            const int j0 = (pf.s.c0 + pf.tile) * kTile + lane * n;
             wanted = j0 < pf.s.len && j0 + n > pf.s.start;
-            if (wanted) page = __ldg(a.block_table + (int64_t)pf.b * a.table_stride + (j0 >> ln));
+            if (wanted) page = __ldg(a.block_table + (int64_t)pf.b * a.table_stride + j0 / n);
         }
     };
-    uint32_t okmask[kStages];   // pages of a stage that hold tokens
     auto issue = [&](int s) {
-        okmask[s] = 0;
         if (have) {
             const bool good = wanted && page >= 0 && page < a.num_pages;
             if (wanted && !good) set_flag(a.flags, MAPLE_DEVFLAG_BAD_INDEX);
             const uint32_t m = __ballot_sync(FULL, good);
-            okmask[s] = m;
+            if (lane == 0) okmask[s] = m;
             const uint32_t bar = bar0 + 8 * s;
             if (lane == 0) {
                 if (m) mbar_expect_tx(bar, __popc(m) * page_bytes);
@@ -247,19 +275,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
             }
             __syncwarp();
             if (good)
-                bulk_g2s(smem_addr(smem + (warp * kStages + s) * L::kTileBytes + lane * page_bytes),
+                bulk_g2s(smem_addr(smem + (ring * kStages + s) * L::kTileBytes + lane * page_bytes),
                          a.pages + ((int64_t)page * a.kv_heads + pf.col / p.HB) * page_bytes, page_bytes, bar);
-            pf.tile += kWarps;
+            pf.tile += kRings;
             settle();
         }
     };
-    settle();
-    uint32_t issued = 0, used = 0;   // tiles of this warp
-#pragma unroll
-    for (int s = 0; s < kStages; s++) {
-        if (have) issued++;
-        issue(s);
+    uint32_t issued = 0, used = 0;   // tiles of this ring
+    if (loader) {
+        settle();
+        for (int s = 0; s < kStages; s++) {
+            if (have) issued++;
+            issue(s);
+        }
     }
+    ring_sync();   // (the masks of the first tiles)
 
     const int heads_per = a.heads / a.kv_heads;
     bool dead = false;
@@ -273,7 +303,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
         if (ntile > 0 || empty) {
             // ---- queries: B fragments, their sums, and the softmax scale of this lane's two heads
             uint32_t qf[NT][G][4];
-            float qs[NT][G][2], qb[NT][G][2], sc[NT][2];
+            uint32_t qs[NT][2];
+            float qb[NT][G][2], sc[NT][2];
 #pragma unroll
             for (int j = 0; j < NT; j++) {
                 const int h = j * 8 + g;
@@ -285,6 +316,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
 #pragma unroll
                     for (int i = 0; i < G; i++) raw[i] = __ldg(reinterpret_cast<const uint4 *>(src + 32 * i));
                 }
+                qs[j][0] = qs[j][1] = 0;
                 float amax = 0.0f;
 #pragma unroll
                 for (int i = 0; i < G; i++) {
@@ -298,8 +330,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
                 // 2^-e with amax * 2^-e in [1, 2) (as far as 2^-e and 2^e are normal); 1 for zero and what is not finite
                 int e = (int)(__float_as_uint(amax) >> 23) - 127;
                 if (e >= 127 || e < -120) e = e == 127 ? 126 : (amax == 0.0f || e == 128 ? 0 : -120);
-                const float down = __int_as_float((127 - e) << 23);
-                float mine_sc = a.scale * 1.4426950408889634f * __int_as_float((127 + e) << 23);
+                const float down = copysignf(__int_as_float((127 - e) << 23), a.scale);
+                // (a negative scale goes into q; 10^-30 is as good as 0 and keeps -inf * scale)
+                const float mine_sc = fmaxf(fabsf(a.scale) * 1.4426950408889634f * __int_as_float((127 + e) << 23), 1e-30f);
 #pragma unroll
                 for (int i = 0; i < G; i++) {
                     float x[8];
@@ -319,11 +352,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
                     sum += __shfl_xor_sync(FULL, sum, 2);
                     bias += __shfl_xor_sync(FULL, bias, 1);
                     bias += __shfl_xor_sync(FULL, bias, 2);
-#pragma unroll
-                    for (int c = 0; c < 2; c++) {
-                        qs[j][i][c] = __shfl_sync(FULL, sum, (2 * t + c) * 4);
-                        qb[j][i][c] = -1024.0f * __shfl_sync(FULL, bias, (2 * t + c) * 4);
+                    if (i == t) {   // rows 2t+1 (the minima of group t) in two fp16 terms, 22 bits
+                        const __half hi = __float2half_rn(sum);
+                        const __half2 h2 = __halves2half2(__float2half_rn(0.0f), hi);
+                        const __half2 l2 = __halves2half2(__float2half_rn(0.0f), __float2half_rn(sum - __half2float(hi)));
+                        qs[j][0] = as_u32(h2);
+                        qs[j][1] = as_u32(l2);
                     }
+#pragma unroll
+                    for (int c = 0; c < 2; c++) qb[j][i][c] = -1024.0f * __shfl_sync(FULL, bias, (2 * t + c) * 4);
                 }
 #pragma unroll
                 for (int c = 0; c < 2; c++) sc[j][c] = __shfl_sync(FULL, mine_sc, (2 * t + c) * 4);
@@ -339,23 +376,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
                 sum[j][0] = sum[j][1] = 0.0f;
             }
 
-            // ---- this warp's tiles of the segment
-            for (int tile = cur.first + warp; tile < cur.last; tile += kWarps) {
+            // ---- this ring's tiles of the segment
+            for (int tile = cur.first + ring; tile < cur.last; tile += kRings) {
                 const int s = used % kStages;
                 if (!dead && !mbar_wait(bar0 + 8 * s, (used / kStages) & 1, abort, a.flags, kDefaultWaitNs)) dead = true;
                 dead = __any_sync(FULL, dead);
-                const uint8_t *buf = smem + (warp * kStages + s) * L::kTileBytes;
-                uint32_t ok = 0;
-#pragma unroll
-                for (int q = 0; q < kStages; q++)
-                    if (q == s) ok = okmask[q];
+                const uint8_t *buf = smem + (ring * kStages + s) * L::kTileBytes;
+                const uint32_t ok = okmask[s];
                 const int j0 = (cur.s.c0 + tile) * kTile;
                 const bool edge = j0 < cur.s.start || j0 + kTile > cur.s.len || ok != (1u << ppt) - 1;
                 if (!dead) {
-                    float S[NT][4][4];
+                    float S[NT][KB][4];
 #pragma unroll
-                    for (int kb = 0; kb < 4; kb++) {
-                        const int pg = (kb * 16) >> ln, r0 = kb * 16 - (pg << ln);
+                    for (int kb = 0; kb < KB; kb++) {
+                        const int k0 = (sub * KB + kb) * 16, pg = k0 / n, r0 = k0 % n;
                         const uint8_t *base = buf + pg * page_bytes;
                         uint32_t w0[G], w1[G], pr0[G], pr1[G];
                         if (G == 4) {
@@ -369,30 +403,33 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
                             *(uint2 *)pr0 = *(const uint2 *)(base + P::k_pair(n, r0 + g, 0));
                             *(uint2 *)pr1 = *(const uint2 *)(base + P::k_pair(n, r0 + g + 8, 0));
                         }
+                        // sum_groups m_g sum(q_g): the (scale, minimum) pairs themselves as the 16-row operand
+                        const uint32_t mp0 = *(const uint32_t *)(base + P::k_pair(n, r0 + g, t % G));
+                        const uint32_t mp1 = *(const uint32_t *)(base + P::k_pair(n, r0 + g + 8, t % G));
 #pragma unroll
-                        for (int j = 0; j < NT; j++) S[j][kb][0] = S[j][kb][1] = S[j][kb][2] = S[j][kb][3] = 0.0f;
+                        for (int j = 0; j < NT; j++) mma16_from(S[j][kb], mp0, mp1, mp0, mp1, qs[j][0], qs[j][1], 0.0f, 0.0f);
 #pragma unroll
                         for (int i = 0; i < G; i++) {
                             const uint32_t a0 = lo_codes(w0[i]), a1 = lo_codes(w1[i]), a2 = hi_codes(w0[i]), a3 = hi_codes(w1[i]);
                             const uint32_t x0 = w0[i] >> 8, x1 = w1[i] >> 8;
                             const uint32_t c0 = lo_codes(x0), c1 = lo_codes(x1), c2 = hi_codes(x0), c3 = hi_codes(x1);
-                            const float2 f0 = __half22float2(as_h2(pr0[i])), f1 = __half22float2(as_h2(pr1[i]));
+                            const float s0 = __low2float(as_h2(pr0[i])), s1 = __low2float(as_h2(pr1[i]));
 #pragma unroll
                             for (int j = 0; j < NT; j++) {
-                                float c[4] = {qb[j][i][0], qb[j][i][1], qb[j][i][0], qb[j][i][1]};
-                                mma16(c, a0, a1, a2, a3, qf[j][i][0], qf[j][i][1]);
+                                float c[4];
+                                mma16_from(c, a0, a1, a2, a3, qf[j][i][0], qf[j][i][1], qb[j][i][0], qb[j][i][1]);
                                 mma16(c, c0, c1, c2, c3, qf[j][i][2], qf[j][i][3]);
-                                S[j][kb][0] = fmaf(f0.x, c[0], fmaf(f0.y, qs[j][i][0], S[j][kb][0]));
-                                S[j][kb][1] = fmaf(f0.x, c[1], fmaf(f0.y, qs[j][i][1], S[j][kb][1]));
-                                S[j][kb][2] = fmaf(f1.x, c[2], fmaf(f1.y, qs[j][i][0], S[j][kb][2]));
-                                S[j][kb][3] = fmaf(f1.x, c[3], fmaf(f1.y, qs[j][i][1], S[j][kb][3]));
+                                S[j][kb][0] = fmaf(s0, c[0], S[j][kb][0]);
+                                S[j][kb][1] = fmaf(s0, c[1], S[j][kb][1]);
+                                S[j][kb][2] = fmaf(s1, c[2], S[j][kb][2]);
+                                S[j][kb][3] = fmaf(s1, c[3], S[j][kb][3]);
                             }
                         }
                         if (edge) {
                             const bool okp = (ok >> pg) & 1;
 #pragma unroll
                             for (int half = 0; half < 2; half++) {
-                                const int key = j0 + kb * 16 + g + 8 * half;
+                                const int key = j0 + k0 + g + 8 * half;
                                 if (!okp || key < cur.s.start || key >= cur.s.len) {
 #pragma unroll
                                     for (int j = 0; j < NT; j++) S[j][kb][2 * half] = S[j][kb][2 * half + 1] = -INFINITY;
@@ -400,37 +437,29 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
                             }
                         }
                     }
-                    // ---- running maximum, weights
+                    // ---- weights 2^(score - reference + 4).  The reference follows the maximum only when a
+                    // score passes it by 2^8 (fp16 holds 2^12), which a vote finds without reducing over the
+                    // lanes; the sums do not depend on it otherwise.
 #pragma unroll
                     for (int j = 0; j < NT; j++) {
-                        float mn[2];
-                        bool moved = false;
+                        float m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                        for (int c = 0; c < 2; c++) {
-                            // (a negative scale turns the order: the maximum is taken of the scaled scores)
-                            float m = -INFINITY;
+                        for (int kb = 0; kb < KB; kb++)
 #pragma unroll
-                            for (int kb = 0; kb < 4; kb++) {
-#pragma unroll
-                                for (int half = 0; half < 2; half++) {
-                                    float &v = S[j][kb][2 * half + c];
-                                    v = v == -INFINITY && edge ? v : v * sc[j][c];
-                                    m = fmaxf(m, v);
-                                }
-                            }
-                            m = fmaxf(m, __shfl_xor_sync(FULL, m, 4));
-                            m = fmaxf(m, __shfl_xor_sync(FULL, m, 8));
-                            m = fmaxf(m, __shfl_xor_sync(FULL, m, 16));
-                            mn[c] = fmaxf(mx[j][c], m);
-                            moved = moved || mn[c] > mx[j][c];
-                        }
-                        if (__any_sync(FULL, moved)) {
+                            for (int c = 0; c < 4; c++) m[c & 1] = fmaxf(m[c & 1], S[j][kb][c]);
+                        const bool above = m[0] * sc[j][0] > mx[j][0] + 8.0f || m[1] * sc[j][1] > mx[j][1] + 8.0f;
+                        if (__any_sync(FULL, above)) {
                             float f[2];
 #pragma unroll
                             for (int c = 0; c < 2; c++) {
-                                f[c] = mx[j][c] == -INFINITY ? 0.0f : ex2(mx[j][c] - mn[c]);
+                                float v = m[c] * sc[j][c];
+                                v = fmaxf(v, __shfl_xor_sync(FULL, v, 4));
+                                v = fmaxf(v, __shfl_xor_sync(FULL, v, 8));
+                                v = fmaxf(v, __shfl_xor_sync(FULL, v, 16));
+                                v = fmaxf(mx[j][c], v);
+                                f[c] = mx[j][c] == -INFINITY ? 0.0f : ex2(mx[j][c] - v);
                                 sum[j][c] *= f[c];
-                                mx[j][c] = mn[c];
+                                mx[j][c] = v;
                             }
 #pragma unroll
                             for (int i = 0; i < MT; i++) {
@@ -442,21 +471,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
                         }
 #pragma unroll
                         for (int c = 0; c < 2; c++) {
-                            const float off = mx[j][c] == -INFINITY ? 0.0f : 8.0f - mx[j][c];
+                            const float off = mx[j][c] == -INFINITY ? 0.0f : 4.0f - mx[j][c];
 #pragma unroll
-                            for (int kb = 0; kb < 4; kb++)
+                            for (int kb = 0; kb < KB; kb++)
 #pragma unroll
                                 for (int half = 0; half < 2; half++) {
                                     float &v = S[j][kb][2 * half + c];
-                                    v = ex2(v + off);
+                                    v = ex2(fmaf(v, sc[j][c], off));
                                     sum[j][c] += v;
                                 }
                         }
                     }
                     // ---- O^T += V^T P^T
 #pragma unroll
-                    for (int kb = 0; kb < 4; kb++) {
-                        const int pg = (kb * 16) >> ln, r0 = kb * 16 - (pg << ln);
+                    for (int kb = 0; kb < KB; kb++) {
+                        const int k0 = (sub * KB + kb) * 16, pg = k0 / n, r0 = k0 % n;
                         const uint8_t *base = buf + pg * page_bytes;
                         const uint8_t *vb = base + n * (D / 2) + (r0 >> 4) * (8 * D) + lane * 16;
                         const int gg = g * (D / 8) / 32;   // the group of this lane's channels
@@ -469,7 +498,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
                             const bool okp = (ok >> pg) & 1;
 #pragma unroll
                             for (int i = 0; i < 4; i++) {
-                                const int key = j0 + kb * 16 + 2 * t + (i & 1) + 8 * (i >> 1);
+                                const int key = j0 + k0 + 2 * t + (i & 1) + 8 * (i >> 1);
                                 if (!okp || key < cur.s.start || key >= cur.s.len) {
                                     const uint32_t keep = (i & 1) ? 0x0000ffffu : 0xffff0000u;
                                     if (i < 2) { s0 &= keep; m0 &= keep; }
@@ -524,12 +553,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
                             }
                     }
                 }
-                __syncwarp();
+                ring_sync();      // all of the ring's warps have read the tile
                 used++;
-                if (have) issued++;
-#pragma unroll
-                for (int q = 0; q < kStages; q++)
-                    if (q == s) issue(q);
+                if (loader) {
+                    if (have) issued++;
+                    issue(s);
+                }
             }
 
             // ---- join the warps: common maximum, then sums in a fixed tree
@@ -569,7 +598,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
                     O[j][i][3] *= f[1];
                 }
             }
-            const int busy = min(kWarps, ntile);    // (warps beyond the tiles hold zeros)
+            const int busy = min(kRings, ntile) * PW;    // (warps beyond the tiles hold zeros)
             for (int m = busy; m > 1;) {
                 const int half = (m + 1) / 2;
                 if (warp >= half && warp < m) {
@@ -646,19 +675,26 @@ __global__ void __launch_bounds__(kWarps * 32, 1) cached_kernel(const CachedK p)
         }
         more = next_segment(cur);
     }
-    for (; used < issued; used++)   // copies still in flight (only after a failed wait)
+    for (; loader && used < issued; used++)   // copies still in flight (only after a failed wait)
         mbar_wait(bar0 + 8 * (used % kStages), (used / kStages) & 1, abort, a.flags, kDefaultWaitNs);
     asm volatile("griddepcontrol.launch_dependents;");
 }
 
-// Joins the partial results of segments that several CTAs share; one CTA per
-// (sequence, column), heads x D/4 threads, partial results in the CTAs' order.
+// Joins the partial results of segments that several CTAs share: one CTA per
+// (sequence, column, head), its 8 warps taking every eighth partial result and
+// summed in order, so that all loads are in flight at once (a loop over the
+// partial results by one thread per output cost 40 us for 75 of them).
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(256) combine_kernel(const CachedK p)
 {
+    constexpr int V = D / 32;      // channels of a lane
+    __shared__ float s_f[kCtas], s_l[8], s_acc[8][D], s_m[8];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const maple_attn_cached_args &a = p.a;
-    const int b = blockIdx.x / p.cols, col = blockIdx.x - b * p.cols;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.x / p.cols, col = blockIdx.x - b * p.cols, h = blockIdx.y;
+    const int heads_per = a.heads / a.kv_heads, kvh = col / p.HB, h0 = (col - kvh * p.HB) * 8 * NT;
+    if (h >= heads_per - h0) return;
     Span s, e;
     s.load(a, b);
     e.load(a, a.B - 1);
@@ -670,30 +706,50 @@ __global__ void __launch_bounds__(256) combine_kernel(const CachedK p)
     auto share = [&](int64_t x) { return (int)(((x + 1) * ns - 1) / total); };
     const int i0 = share(W + kSegCost), i1 = share(W + kSegCost + s.n - 1);
     if (i0 == i1) return;
-    const int heads_per = a.heads / a.kv_heads, kvh = col / p.HB, h0 = (col - kvh * p.HB) * 8 * NT;
-    const int nh = min(8 * NT, heads_per - h0);
-    auto slot = [&](int i) { return 2 * i + (total * i / ns >= W ? 0 : 1); };
-    for (int x = threadIdx.x; x < nh * (D / 4); x += blockDim.x) {
-        const int h = x / (D / 4), c = x - h * (D / 4);
-        float m = -INFINITY;
-        for (int i = i0; i <= i1; i++) m = fmaxf(m, p.part_ml[((int64_t)slot(i) * 8 * NT + h) * 2]);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.0f;
+    const int first_slot = 2 * i0 + (total * i0 / ns >= W ? 0 : 1);   // (later shares begin inside the segment)
+    auto at = [&](int i) { return (int64_t)(i == i0 ? first_slot : 2 * i) * 8 * NT + h; };
+    // factors of the partial results
+    const int np = i1 - i0 + 1;
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if ((int)threadIdx.x < np) ml = *reinterpret_cast<const float2 *>(p.part_ml + at(i0 + threadIdx.x) * 2);
+    const float wm = warp_max(ml.x);
+    if (lane == 0) s_m[warp] = wm;
+    __syncthreads();
+    float m = s_m[0];
+#pragma unroll
+    for (int w = 1; w < 8; w++) m = fmaxf(m, s_m[w]);
+    const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
+    if ((int)threadIdx.x < np) s_f[threadIdx.x] = f;
+    const float wl = warp_tree_sum(f * ml.y);
+    if (lane == 0) s_l[warp] = wl;
+    __syncthreads();
+    float acc[V];
+#pragma unroll
+    for (int v = 0; v < V; v++) acc[v] = 0.0f;
 #pragma unroll 4
-        for (int i = i0; i <= i1; i++) {
-            const int64_t at = (int64_t)slot(i) * 8 * NT + h;
-            const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + at * 2);
-            const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
-            const float4 v = *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * c);
-            l = fmaf(ml.y, f, l);
-            acc.x = fmaf(v.x, f, acc.x);
-            acc.y = fmaf(v.y, f, acc.y);
-            acc.z = fmaf(v.z, f, acc.z);
-            acc.w = fmaf(v.w, f, acc.w);
+    for (int i = warp; i < np; i += 8) {
+        const float *src = p.part_o + at(i0 + i) * D + V * lane;
+        const float fi = s_f[i];
+        float x[V];
+        if (V == 4) *(float4 *)x = *reinterpret_cast<const float4 *>(src);
+        else *(float2 *)x = *reinterpret_cast<const float2 *>(src);
+#pragma unroll
+        for (int v = 0; v < V; v++) acc[v] = fmaf(x[v], fi, acc[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < V; v++) s_acc[warp][V * lane + v] = acc[v];
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+        float l = 0.0f, x0 = 0.0f, x1 = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; w++) {
+            l += s_l[w];
+            x0 += s_acc[w][2 * threadIdx.x];
+            x1 += s_acc[w][2 * threadIdx.x + 1];
         }
         const float inv = l > 0.0f || l != l ? __fdiv_rn(1.0f, l) : 0.0f;
-        uint2 o = make_uint2(Elem<T>::pack(acc.x * inv, acc.y * inv), Elem<T>::pack(acc.z * inv, acc.w * inv));
-        *reinterpret_cast<uint2 *>((T *)a.out + ((int64_t)b * a.heads + kvh * heads_per + h0 + h) * D + 4 * c) = o;
+        reinterpret_cast<uint32_t *>((T *)a.out + ((int64_t)b * a.heads + kvh * heads_per + h0 + h) * D)[threadIdx.x] =
+            Elem<T>::pack(x0 * inv, x1 * inv);
     }
 }
 
@@ -721,17 +777,20 @@ Plan make_plan(int32_t B, int32_t max_pages, int32_t heads, int32_t kv_heads, in
 template <typename T, int D, int NT>
 int launch(const CachedK &k, cudaStream_t st)
 {
-    const int smem = CachedSmem<D>::total(NT);
-    if (cudaFuncSetAttribute(cached_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    const int smem = CachedSmem<D, NT>::kTotal;
+    auto kernel = k.a.page_size == 16   ? cached_kernel<T, D, NT, 16>
+                  : k.a.page_size == 32 ? cached_kernel<T, D, NT, 32>
+                                        : cached_kernel<T, D, NT, 64>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
         cudaGetLastError();
         return MAPLE_ERR_CUDA;
     }
     const int64_t segments = (int64_t)k.a.B * k.cols;
-    cached_kernel<T, D, NT><<<(unsigned)(k.whole ? segments : kCtas), kWarps * 32, smem, st>>>(k);
+    kernel<<<(unsigned)(k.whole ? segments : kCtas), CachedSmem<D, NT>::kWarps * 32, smem, st>>>(k);
     if (!k.whole) {
         cudaLaunchConfig_t lc;
         memset(&lc, 0, sizeof lc);
-        lc.gridDim = dim3((unsigned)segments);
+        lc.gridDim = dim3((unsigned)segments, 8 * NT);
         lc.blockDim = dim3(256);
         lc.stream = st;
         cudaLaunchAttribute attr[1];
