@@ -19,7 +19,10 @@
 //   warp 9    MMA: S_A = Q_A K_0, S_B = Q_B K_0, then per key tile j
 //             O_A += P_A V_j, S_A = Q_A K_j+1, O_B += P_B V_j, S_B = Q_B K_j+1
 //   warps 0-3 softmax of A, warps 4-7 of B: one thread per row, S from tensor
-//             memory, P back over the same columns; rescaling and the epilogue
+//             memory, P back over the same columns, handed over in two halves;
+//             rescaling and the epilogue
+//   warp 10   the CTA's items, one ahead: the loads and first products of the
+//             next item run under the last softmax and epilogue of this one
 // While one tile's rows are in the exponentials, the tensor cores work on the
 // other's products.  Tensor memory: S_A, S_B (P over their first half), O_A,
 // O_B = 512 columns at d = 128.  In-order execution of the MMAs makes "S_j full"
@@ -31,7 +34,8 @@
 // those values add them again at the end.
 //
 // Work is ordered from the last tokens (the longest rows) to the first, so that
-// the short items fill the end of the run.
+// the short items fill the end of the run; CTAs that are done take over blocks
+// that have not started (cluster launch control).
 #include <cuda.h>
 #include <math.h>
 #include <stdint.h>
@@ -47,7 +51,7 @@ namespace {
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 // three warpgroups: two of softmax rows, one of which two warps work; the
-// launch's 384 x 168 registers are shared out as 2 x 128 x 216 + 128 x 72
+// launch's 384 x 168 registers are shared out as 2 x 128 x 208 + 128 x 88
 constexpr int kThreads = 384;
 constexpr int kKeys = 128;   // keys of a tile
 
@@ -130,6 +134,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// one lane of the warp, the same every time
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // the bits of the two 16-bit halves of w that hold an infinity or NaN
 template <typename T>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w)
@@ -137,6 +149,107 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w)
     constexpr uint32_t E = sizeof(T) && __is_same(T, __nv_bfloat16) ? 0x7f80u : 0x7c00u;
     return ((w & E) == E ? 0xffffu : 0u) | ((w & (E << 16)) == (E << 16) ? 0xffff0000u : 0u);
 }
+
+// Cluster launch control: a running CTA takes over one that has not started, so
+// that items are handed out as CTAs get free, without a counter in memory.
+__device__ __forceinline__ void try_cancel(uint32_t dst, uint32_t bar)
+{
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+                 "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ int cancelled_block(const uint4 *resp)   // its blockIdx.x, or -1
+{
+    int x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b64 lo, hi;\n\t"
+        "ld.shared.v2.b64 {lo, hi}, [%1];\n\t"
+        "mov.b128 r, {lo, hi};\n\t"
+        "mov.s32 %0, -1;\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+        : "=r"(x)
+        : "r"(smem_addr(resp))
+        : "memory");
+    return x;
+}
+
+// An item: a pair of tiles of one sequence and key/value head
+struct Item {
+    int kvh, tA, q0, lq, k0, off;      // kvh < 0: no more
+};
+
+// The item of a block: (sequence, pair) in the order of the sequences from the
+// last one, a sequence's pairs from its last tokens, key/value heads fastest.
+// One warp; 32 sequences at a time.  kvh = -2: beyond the last item.
+__device__ __forceinline__ Item find_item(const maple_attn_prompt_args &a, int nt, int block)
+{
+    const int lane = threadIdx.x & 31, span = 2 * nt;
+    Item it;
+    it.kvh = -2;
+    const int x = block / a.kv_heads;
+    int at = 0;
+    for (int b0 = a.B - 1; b0 >= 0; b0 -= 32) {
+        const int b = b0 - lane;
+        int n = 0;
+        int64_t q0 = 0, q1 = 0, qfull = 0;
+        if (b >= 0) {
+            const int64_t u = __ldg(a.cu_q + b), v = __ldg(a.cu_q + b + 1);
+            q0 = min(max(u, (int64_t)0), a.Tq);
+            qfull = q1 = min(max(v, q0), a.Tq);
+            q1 = min(q1, q0 + a.max_q);
+            n = (int)((q1 - q0 + span - 1) / span);
+        }
+        int inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(FULL, inc, o);
+            if (lane >= o) inc += v;
+        }
+        const int from = at + inc - n;
+        const unsigned hit = __ballot_sync(FULL, x >= from && x < from + n);
+        if (hit) {
+            int64_t k0 = 0, k1 = 0;
+            if (b >= 0) {
+                k0 = min(max((int64_t)__ldg(a.cu_k + b), (int64_t)0), a.Tk);
+                k1 = min(max((int64_t)__ldg(a.cu_k + b + 1), k0), a.Tk);
+            }
+            const int src = __ffs(hit) - 1;
+            it.kvh = block - x * a.kv_heads;
+            it.tA = __shfl_sync(FULL, (n - 1 - (x - from)) * span, src);
+            it.q0 = __shfl_sync(FULL, (int)q0, src);
+            it.lq = __shfl_sync(FULL, (int)(q1 - q0), src);
+            it.k0 = __shfl_sync(FULL, (int)k0, src);
+            it.off = __shfl_sync(FULL, (int)((k1 - k0) - (qfull - q0)), src);   // (a cut by max_q moves no position)
+            return it;
+        }
+        at += __shfl_sync(FULL, inc, 31);
+    }
+    return it;
+}
+
+// What the roles derive from an item
+struct Range {
+    int tB, last, kbeg, n;
+    bool hasB;
+    __device__ __forceinline__ Range(const Item &it, int nt, int window)
+    {
+        tB = it.tA + nt;
+        hasB = tB < it.lq;
+        last = min(it.tA + 2 * nt, it.lq) - 1;                   // last query token of the pair
+        kbeg = window ? max(it.tA + it.off - window + 1, 0) : 0;
+        const int kend = last + it.off + 1;
+        n = kend > kbeg ? (kend - kbeg + kKeys - 1) / kKeys : 0;   // tiles of keys
+    }
+    // whether some row of the pair does not see all keys of tile j
+    __device__ __forceinline__ bool masked(const Item &it, int window, int j) const
+    {
+        const int s = kbeg + j * kKeys;
+        return s + kKeys - 1 > it.tA + it.off || (window && s < last + it.off - window + 1);
+    }
+};
+
+constexpr int kItems = 2;   // items in hand: the one being worked on and the next
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -146,8 +259,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     using L = PromptSmem<D>;
     constexpr int S = L::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ int s_item[8];
-    __shared__ int s_warp[kThreads / 32];
+    __shared__ Item s_items[kItems];
+    __shared__ __align__(16) uint4 s_cancel;
     const maple_attn_prompt_args &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (smem_addr(smem) & 1023u) {   // the swizzled tiles need 1024-byte alignment
@@ -155,292 +268,369 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         return;
     }
     uint64_t *bars = (uint64_t *)(smem + L::kBars);
-    const uint32_t b_full = smem_addr(bars), b_empty = b_full + 8 * S, b_q = b_empty + 8 * S;
-    const uint32_t b_s = b_q + 8, b_p = b_s + 16, b_o = b_p + 16, b_drain = b_o + 16;
-    uint32_t *tmem_holder = (uint32_t *)(bars + 2 * S + 8);
+    const uint32_t b_full = smem_addr(bars), b_empty = b_full + 8 * S, b_q = b_empty + 8 * S, b_qfree = b_q + 8;
+    const uint32_t b_s = b_qfree + 8, b_p = b_s + 16, b_o = b_p + 32, b_item = b_o + 16, b_ifree = b_item + 8 * kItems;
+    const uint32_t b_cancel = b_ifree + 8 * kItems, b_drain = b_cancel + 8, b_next = b_drain + 8;
+    uint32_t *tmem_holder = (uint32_t *)(bars + 2 * S + 2 + 2 + 4 + 2 + 2 * kItems + 3);
     volatile uint32_t *abort = tmem_holder + 1;
-    uint32_t *odd_values = tmem_holder + 2;   // something in V was not finite
+    uint32_t *odd_values = tmem_holder + 2;   // [2 items] something in V was not finite
+    const uint64_t limit = kDefaultWaitNs;
 
-    // ---- this CTA's item: sequence, pair of tiles; items lie sequence by
-    // sequence, taken from the end
-    const int span = 2 * p.nt;
-    const int item_kv = blockIdx.x % a.kv_heads, kvh = item_kv;
-    const int x = blockIdx.x / a.kv_heads;
-    auto bounds = [&](int b, int64_t &q0, int64_t &q1, bool &bad) {
-        const int64_t u = __ldg(a.cu_q + b), v = __ldg(a.cu_q + b + 1);
-        q0 = min(max(u, (int64_t)0), a.Tq);
-        q1 = min(max(v, q0), a.Tq);
-        bad = q0 != u || q1 != v || q1 - q0 > a.max_q;
-        q1 = min(q1, q0 + a.max_q);
-    };
     if (threadIdx.x == 0) {
-        s_item[0] = -1;
         for (int s = 0; s < S; s++) {
             mbar_init(b_full + 8 * s, 1);
             mbar_init(b_empty + 8 * s, 1);
         }
         mbar_init(b_q, 1);
+        mbar_init(b_qfree, 1);
         for (int i = 0; i < 2; i++) {
             mbar_init(b_s + 8 * i, 1);
-            mbar_init(b_p + 8 * i, 4);
+            mbar_init(b_p + 16 * i, 4);       // first half of P
+            mbar_init(b_p + 16 * i + 8, 4);   // second half
             mbar_init(b_o + 8 * i, 1);
         }
+        for (int i = 0; i < kItems; i++) {
+            mbar_init(b_item + 8 * i, 1);
+            mbar_init(b_ifree + 8 * i, 10);   // loads, products, 8 softmax warps
+            odd_values[i] = 0u;
+        }
+        mbar_init(b_cancel, 1);
         mbar_init(b_drain, 1);
+        mbar_init(b_next, 1);
         *abort = 0u;
-        *odd_values = 0u;
         fence_barrier_init();
     }
-    // count the pairs from the last sequence on; the thread whose stretch of sequences holds item x finds it
-    {
-        const int per = (a.B + kThreads - 1) / kThreads;
-        const int hi = a.B - min((int)threadIdx.x * per, a.B), lo = max(hi - per, 0);
-        int mine = 0;
-        for (int b = hi - 1; b >= lo; b--) {
-            int64_t q0, q1;
-            bool bad;
-            bounds(b, q0, q1, bad);
-            mine += (int)((q1 - q0 + span - 1) / span);
-        }
-        int inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(FULL, inc, o);
-            if (lane >= o) inc += v;
-        }
-        if (lane == 31) s_warp[warp] = inc;
-        __syncthreads();
-        int at = inc - mine;
-        for (int w = 0; w < warp; w++) at += s_warp[w];
-        if (x >= at && x < at + mine) {
-            for (int b = hi - 1; b >= lo; b--) {
-                int64_t q0, q1;
-                bool bad;
-                bounds(b, q0, q1, bad);
-                const int n = (int)((q1 - q0 + span - 1) / span);
-                if (x >= at && x < at + n) {
-                    const int64_t ku = __ldg(a.cu_k + b), kv = __ldg(a.cu_k + b + 1);
-                    const int64_t k0 = min(max(ku, (int64_t)0), a.Tk), k1 = min(max(kv, k0), a.Tk);
-                    s_item[0] = n - 1 - (x - at);   // the last tokens first
-                    s_item[1] = (int)q0;
-                    s_item[2] = (int)(q1 - q0);
-                    s_item[3] = (int)k0;
-                    s_item[4] = (int)(k1 - k0);
-                    // (the cut of max_q does not move the queries' positions)
-                    s_item[5] = (int)((k1 - k0) - (min(max((int64_t)__ldg(a.cu_q + b + 1), q0), a.Tq) - q0));
-                }
-                at += n;
-            }
-        }
-        if (blockIdx.x == 0) {   // report offsets that were cut
-            for (int b = hi - 1; b >= lo; b--) {
-                int64_t q0, q1;
-                bool bad;
-                bounds(b, q0, q1, bad);
-                const int64_t ku = __ldg(a.cu_k + b), kv = __ldg(a.cu_k + b + 1);
-                if (bad || ku < 0 || kv < ku || kv > a.Tk) set_flag(a.flags, MAPLE_DEVFLAG_BAD_INDEX);
-            }
-        }
-    }
-    __syncthreads();
-    const int pair = s_item[0];
-    if (pair < 0) return;       // beyond the last item
-    const int q0 = s_item[1], lq = s_item[2], k0 = s_item[3], off = s_item[5];
-    const int tA = pair * span, tB = tA + p.nt;
-    const bool hasB = tB < lq;
-    const int last = min(tA + span, lq) - 1;               // last query token of the pair
-    const int kbeg = a.window ? max(tA + off - a.window + 1, 0) : 0, kend = last + off + 1;
-    const int n = kend > kbeg ? (kend - kbeg + kKeys - 1) / kKeys : 0;   // tiles of keys
-    // whether some row of the pair does not see all keys of tile j
-    auto masked = [&](int j) {
-        const int s = kbeg + j * kKeys;
-        return s + kKeys - 1 > tA + off || (a.window && s < last + off - a.window + 1);
-    };
-
     if (warp == 9) tmem_alloc(smem_addr(tmem_holder), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     constexpr uint32_t kO = 256;   // first column of O_A
+
+    // the u-th item of this CTA, as the scheduling warp wrote it (false: a wait gave up)
+    auto get_item = [&](int u, Item &it) -> bool {
+        const int s = u % kItems;
+        if (!mbar_wait(b_item + 8 * s, (u / kItems) & 1, abort, a.flags, limit)) return false;
+        it = s_items[s];
+        return true;
+    };
+    auto drop_item = [&](int u) { mbar_arrive(b_ifree + 8 * (u % kItems)); };   // by one lane of each reading warp
+
     if (warp >= 8) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-      if (warp == 8) {
-        // ---------------- loads
-        if (lane == 0 && n > 0) {
-            mbar_expect_tx(b_q, (hasB ? 2 : 1) * L::kHalves * p.G * p.nt * 128);
-            for (int i = 0; i < (hasB ? 2 : 1); i++)
-                for (int h = 0; h < L::kHalves; h++)
-                    tma_load_3d(smem_addr(smem + i * L::kTileBytes + h * 16384), &q_map, 64 * h, kvh * p.G, q0 + (i ? tB : tA), b_q);
-            int it = 0;
-            bool ok = true;
-            for (; it < 2 * n; it++) {
-                const int s = it % S;
-                if (!mbar_wait(b_empty + 8 * s, ((it / S) & 1) ^ 1, abort, a.flags, kDefaultWaitNs)) {
-                    ok = false;
-                    break;
+      if (warp == 10) {
+        // ---------------- items: this block's own, then those of blocks that have not started
+        int block = blockIdx.x;
+        bool ok = true;
+        for (int u = 0; ok; u++) {
+            Item it;
+            it.kvh = -1;
+            if (block >= 0) it = find_item(a, p.nt, block);
+            if (block == 0) {   // report offsets that are cut
+                for (int b = lane; b < a.B; b += 32) {
+                    const int64_t q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
+                    if (q0 < 0 || q1 < q0 || q1 > a.Tq || q1 - q0 > a.max_q || k0 < 0 || k1 < k0 || k1 > a.Tk)
+                        set_flag(a.flags, MAPLE_DEVFLAG_BAD_INDEX);
                 }
-                mbar_expect_tx(b_full + 8 * s, L::kTileBytes);
-                for (int h = 0; h < L::kHalves; h++)
-                    tma_load_3d(smem_addr(smem + L::kKv + s * L::kTileBytes + h * 16384), (it & 1) ? &v_map : &k_map, 64 * h, kvh,
-                                k0 + kbeg + (it >> 1) * kKeys, b_full + 8 * s);
             }
-            if (!ok) {   // drain the copies in flight
-                for (int j = it > S ? it - S : 0; j < it; j++) {
-                    const uint64_t t0 = global_ns();
-                    while (!mbar_test(b_full + 8 * (j % S), (j / S) & 1) && global_ns() - t0 < kDefaultWaitNs) {
+            const int s = u % kItems;
+            ok = mbar_wait(b_ifree + 8 * s, ((u / kItems) & 1) ^ 1, abort, a.flags, limit);
+            ok = __all_sync(FULL, ok);
+            if (lane == 0 && ok) {
+                s_items[s] = it;
+                odd_values[s] = 0u;
+                mbar_arrive(b_item + 8 * s);
+            }
+            if (block < 0 || !ok) break;
+            // The next item is asked for when the last load of this one is issued: a whole item
+            // ahead, the order of the items and not the CTAs' progress would decide who gets which.
+            if (!__all_sync(FULL, mbar_wait(b_next, u & 1, abort, a.flags, limit))) break;
+            if (lane == 0) {
+                mbar_expect_tx(b_cancel, 16);
+                try_cancel(smem_addr(&s_cancel), b_cancel);
+            }
+            // (waited for even after a failure: nothing may be in flight at the end)
+            const uint64_t c0 = global_ns();
+            bool got;
+            while (!(got = mbar_test(b_cancel, u & 1)) && global_ns() - c0 < limit) {
+            }
+            block = __all_sync(FULL, got) ? cancelled_block(&s_cancel) : -1;
+            __syncwarp();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the answer is read before it is overwritten
+        }
+      } else if (warp == 8) {
+        // ---------------- loads
+        // One flat loop over all tiles of all items, here and in the products: the ring position
+        // then stays a loop counter that the compiler keeps in uniform registers, where the copies'
+        // and products' operands have to be (moving them there cost a fifth of the kernel's time).
+        if (lane == 0) {
+            Item w;
+            int u = -1, j = 0, n = 0, nq = 0, kbeg = 0;
+            bool ok = true;
+            uint32_t it = 0;
+            for (;; it++, j++) {   // tiles K_j and V_j, ring positions 2 it and 2 it + 1
+                bool done = false;
+                while (j == n) {
+                    if (u >= 0) {
+                        drop_item(u);
+                        mbar_arrive(b_next);
+                    }
+                    u++;
+                    if (!(ok = get_item(u, w)) || w.kvh == -1) {
+                        done = true;
+                        break;
+                    }
+                    const Range g(w, p.nt, a.window);
+                    j = 0;
+                    n = w.kvh >= 0 ? g.n : 0;
+                    kbeg = g.kbeg;
+                    if (n > 0) {
+                        if (!(ok = mbar_wait(b_qfree, (nq & 1) ^ 1, abort, a.flags, limit))) {
+                            done = true;
+                            break;
+                        }
+                        nq++;
+                        mbar_expect_tx(b_q, (g.hasB ? 2 : 1) * L::kHalves * p.G * p.nt * 128);
+                        for (int i = 0; i < (g.hasB ? 2 : 1); i++)
+                            for (int h = 0; h < L::kHalves; h++)
+                                tma_load_3d(smem_addr(smem + i * L::kTileBytes + h * 16384), &q_map, 64 * h, w.kvh * p.G,
+                                            w.q0 + (i ? g.tB : w.tA), b_q);
                     }
                 }
-                const uint64_t t0 = global_ns();
-                while (!mbar_test(b_q, 0) && global_ns() - t0 < kDefaultWaitNs) {
+                if (done) break;
+#pragma unroll
+                for (int kv = 0; kv < 2; kv++) {
+                    const uint32_t t = 2 * it + kv, s = t % S;
+                    if (!(ok = ok && mbar_wait(b_empty + 8 * s, ((t / S) & 1) ^ 1, abort, a.flags, limit))) break;
+                    mbar_expect_tx(b_full + 8 * s, L::kTileBytes);
+                    for (int h = 0; h < L::kHalves; h++)
+                        tma_load_3d(smem_addr(smem + L::kKv + s * L::kTileBytes + h * 16384), kv ? &v_map : &k_map, 64 * h, w.kvh,
+                                    w.k0 + kbeg + j * kKeys, b_full + 8 * s);
+                }
+                if (!ok) break;
+            }
+            if (*abort) {   // drain the copies in flight: whatever was asked of a barrier arrives or runs out of time
+                for (int q = 0; q < S + 1; q++) {
+                    const uint32_t bar = q < S ? b_full + 8 * q : b_q;
+                    const uint64_t c0 = global_ns();
+                    while (global_ns() - c0 < 20000000ull && !(mbar_test(bar, 0) && mbar_test(bar, 1))) {
+                    }
                 }
             }
         }
       } else if (warp == 9) {
         // ---------------- products
-        if (lane == 0 && n > 0) {
-            const bool bf = __is_same(T, __nv_bfloat16);
-            const uint32_t id_s = idesc_f16(bf, kKeys, false), id_o = idesc_f16(bf, D, true);
-            bool ok = mbar_wait(b_q, 0, abort, a.flags, kDefaultWaitNs);
-            auto wait_tile = [&](int it) { return mbar_wait(b_full + 8 * (it % S), (it / S) & 1, abort, a.flags, kDefaultWaitNs); };
-            auto scores = [&](int i, int j) {   // S_i = Q_i K_j^T
-                const uint32_t kb = smem_addr(smem + L::kKv + ((2 * j) % S) * L::kTileBytes);
-                const uint64_t da = desc_sw128(smem_addr(smem + i * L::kTileBytes)), db = desc_sw128(kb);
+        // The whole warp runs this with values that are the same in every lane (votes, broadcasts,
+        // loop counters), and one lane issues: the operands of the products then stay in uniform
+        // registers.  With one lane running it all they were moved there one by one, and issuing
+        // them was what the kernel waited for.
+        const bool leader = elect_one();
+        const bool bf = __is_same(T, __nv_bfloat16);
+        const uint32_t id_s = idesc_f16(bf, kKeys, false), id_o = idesc_f16(bf, D, true);
+        const uint32_t tm = __shfl_sync(FULL, tmem, 0);
+        const uint64_t dq = desc_sw128(smem_addr(smem)), dk = desc_sw128(smem_addr(smem + L::kKv)), dv = desc_mn_sw128(smem_addr(smem + L::kKv));
+        constexpr uint64_t kStep = L::kTileBytes / 16;   // a tile in descriptor units
+        int u = -1, j = 0, n = 0, ni = 0;
+        uint32_t it = 0, phB = 0, nq = 0;      // tiles so far (the phase of P_A), tiles with a B, items with a Q
+        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(FULL, mbar_wait(bar, parity, abort, a.flags, limit)); };
+        auto commit = [&](uint32_t bar) {
+            if (leader) mma_commit(bar);
+            __syncwarp();
+        };
+        // S_i = Q_i K^T of stage s; O_i += P_i V, 64 keys of the V of stage s
+        auto scores = [&](int i, uint32_t s) {
+            const uint64_t da = dq + i * kStep, db = dk + s * kStep;
+            if (leader) {
 #pragma unroll
                 for (int k = 0; k < D / 16; k++)
-                    mma_ss(tmem + 128 * i, da + (k / 4) * 1024 + 2 * (k % 4), db + (k / 4) * 1024 + 2 * (k % 4), id_s, k != 0);
+                    mma_ss(tm + 128 * i, da + (k / 4) * 1024 + 2 * (k % 4), db + (k / 4) * 1024 + 2 * (k % 4), id_s, k != 0);
                 mma_commit(b_s + 8 * i);
-            };
-            auto values = [&](int i, int j) {   // O_i += P_i V_j
-                const uint64_t db = desc_mn_sw128(smem_addr(smem + L::kKv + ((2 * j + 1) % S) * L::kTileBytes));
+            }
+            __syncwarp();
+        };
+        auto values = [&](int i, uint32_t s, int half, bool first) {
+            const uint64_t db = dv + s * kStep;
+            if (leader) {
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; k++)
-                    mma_ts(tmem + kO + D * i, tmem + 128 * i + 8 * k, db + 128 * k, id_o, (j | k) != 0);
-            };
-            const int ni = hasB ? 2 : 1;
-            if (ok && (ok = wait_tile(0))) {
-                tc_fence_after();
-                for (int i = 0; i < ni; i++) scores(i, 0);
-                mma_commit(b_empty);
+                for (int k = 4 * half; k < 4 * half + 4; k++)
+                    mma_ts(tm + kO + D * i, tm + 128 * i + 8 * k, db + 128 * k, id_o, k > 0 || !first);
             }
-            for (int j = 0; ok && j < n; j++) {
-                ok = wait_tile(2 * j + 1) && (j + 1 == n || wait_tile(2 * j + 2));
-                for (int i = 0; ok && i < ni; i++) {
-                    if (!(ok = mbar_wait(b_p + 8 * i, j & 1, abort, a.flags, kDefaultWaitNs))) break;
-                    tc_fence_after();
-                    values(i, j);
-                    if (j + 1 < n) scores(i, j + 1);
-                    else mma_commit(b_o + 8 * i);
+            __syncwarp();
+        };
+        for (;; it++, j++) {
+            bool done = false;
+            while (j == n) {
+                if (u >= 0 && leader) drop_item(u);
+                u++;
+                Item w;
+                const bool got = get_item(u, w);
+                if (!__all_sync(FULL, got) || __shfl_sync(FULL, w.kvh, 0) == -1) {
+                    done = true;
+                    break;
                 }
-                mma_commit(b_empty + 8 * ((2 * j + 1) % S));
-                if (j + 1 < n) mma_commit(b_empty + 8 * ((2 * j + 2) % S));
+                const Range g(w, p.nt, a.window);
+                j = 0;
+                n = __shfl_sync(FULL, w.kvh >= 0 ? g.n : 0, 0);
+                ni = __shfl_sync(FULL, g.hasB ? 2 : 1, 0);
             }
-            mma_commit(b_drain);   // every issued MMA has finished before tensor memory is released
-            const uint64_t t0 = global_ns();
-            while (!mbar_test(b_drain, 0) && global_ns() - t0 < kDefaultWaitNs) {
+            if (done) break;
+            const uint32_t tk = 2 * it, tv = tk + 1, tn = tk + 2;     // ring positions of K_j, V_j and K_j+1
+            if (j == 0) {
+                if (!wait(b_q, nq & 1) || !wait(b_full + 8 * (tk % S), (tk / S) & 1)) break;
+                nq++;
+                tc_fence_after();
+                scores(0, tk % S);
+                if (ni == 2) scores(1, tk % S);
+                commit(b_empty + 8 * (tk % S));
+                if (n == 1) commit(b_qfree);
             }
+            const bool more = j + 1 < n;
+            if (!wait(b_full + 8 * (tv % S), (tv / S) & 1) || (more && !wait(b_full + 8 * (tn % S), (tn / S) & 1))) break;
+            bool ok = true;
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                if (i == 0 || ni == 2) {
+#pragma unroll
+                    for (int half = 0; half < 2; half++) {
+                        ok = ok && wait(b_p + 16 * i + 8 * half, (i == 0 ? it : phB) & 1);
+                        if (ok) {
+                            tc_fence_after();
+                            values(i, tv % S, half, j == 0);
+                        }
+                    }
+                    if (ok) {
+                        if (more) scores(i, tn % S);
+                        else commit(b_o + 8 * i);
+                    }
+                }
+            }
+            if (ni == 2) phB++;
+            if (!ok) break;
+            commit(b_empty + 8 * (tv % S));
+            if (more) commit(b_empty + 8 * (tn % S));
+            if (j + 2 == n) commit(b_qfree);   // the last scores are issued
+        }
+        commit(b_drain);   // every issued MMA has finished before tensor memory is released
+        const uint64_t c0 = global_ns();
+        while (!mbar_test(b_drain, 0) && global_ns() - c0 < limit) {
         }
       }
     } else {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-      if (warp < 4 || hasB) {
-        // ---------------- softmax and epilogue: one thread per row
-        const int i = warp >> 2, r = threadIdx.x & 127;
-        const int tok = (i ? tB : tA) + r / p.G, h = r % p.G;
-        const bool valid = r < p.G * p.nt && tok < lq;
-        const int pos = tok + off;                    // key position of the row's query
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + 128 * i + lanes, to = tmem + kO + D * i + lanes;
-        const bool neg = a.scale < 0.0f;
-        const float scale2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);   // (0 as 10^-30: -inf stays -inf)
-        float m = -INFINITY, l = 0.0f;
-        bool ok = true;
-        for (int j = 0; j < n; j++) {
-            const bool edge = masked(j);
-            if (edge && i == 0) {
-                // V_j: what is not finite becomes 0 before the products read it
-                if (!mbar_wait(b_full + 8 * ((2 * j + 1) % S), ((2 * j + 1) / S) & 1, abort, a.flags, kDefaultWaitNs)) ok = false;
-                if (ok) {
-                    uint4 *tile = (uint4 *)(smem + L::kKv + ((2 * j + 1) % S) * L::kTileBytes);
-                    bool any = false;
+      // ---------------- softmax and epilogue: one thread per row
+      const int i = warp >> 2, r = threadIdx.x & 127;
+      const int rt = r / p.G, h = r - rt * p.G;
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t ts = tmem + 128 * i + lanes, to = tmem + kO + D * i + lanes;
+      const bool neg = a.scale < 0.0f;
+      const float scale2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);   // (0 as 10^-30: -inf stays -inf)
+      int t0 = 0;                 // ring position of the item's K_0
+      uint32_t ns = 0, no = 0;    // phases of S_i and O_i
+      bool ok = true;
+      for (int u = 0; ok; u++) {
+        Item w;
+        if (!(ok = __all_sync(FULL, get_item(u, w))) || w.kvh == -1) break;
+        const Range g(w, p.nt, a.window);
+        const int n = w.kvh >= 0 ? g.n : 0;
+        if (w.kvh >= 0 && (i == 0 || g.hasB)) {
+            const int tok = (i ? g.tB : w.tA) + rt;
+            const bool valid = r < p.G * p.nt && tok < w.lq;
+            const int pos = tok + w.off;                    // key position of the row's query
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < n; j++) {
+                const bool edge = g.masked(w, a.window, j);
+                if (edge && i == 0) {
+                    // V_j: what is not finite becomes 0 before the products read it
+                    const int t = t0 + 2 * j + 1;
+                    if (!mbar_wait(b_full + 8 * (t % S), (t / S) & 1, abort, a.flags, limit)) ok = false;
+                    if (ok) {
+                        uint4 *tile = (uint4 *)(smem + L::kKv + (t % S) * L::kTileBytes);
+                        bool any = false;
 #pragma unroll 4
-                    for (int c = threadIdx.x; c < L::kTileBytes / 16; c += 128) {
-                        const uint4 v = tile[c];
-                        const uint32_t e0 = not_finite<T>(v.x), e1 = not_finite<T>(v.y), e2 = not_finite<T>(v.z), e3 = not_finite<T>(v.w);
-                        if (e0 | e1 | e2 | e3) {
-                            tile[c] = make_uint4(v.x & ~e0, v.y & ~e1, v.z & ~e2, v.w & ~e3);
-                            any = true;
+                        for (int c = threadIdx.x; c < L::kTileBytes / 16; c += 128) {
+                            const uint4 v = tile[c];
+                            const uint32_t e0 = not_finite<T>(v.x), e1 = not_finite<T>(v.y), e2 = not_finite<T>(v.z), e3 = not_finite<T>(v.w);
+                            if (e0 | e1 | e2 | e3) {
+                                tile[c] = make_uint4(v.x & ~e0, v.y & ~e1, v.z & ~e2, v.w & ~e3);
+                                any = true;
+                            }
+                        }
+                        if (any) atomicOr(odd_values + u % kItems, 1u);
+                        fence_async_smem();
+                        // (the products wait for all four warps' halves of P, so for all of the tile)
+                    }
+                }
+                ok = ok && mbar_wait(b_s + 8 * i, ns & 1, abort, a.flags, limit);
+                ok = __all_sync(FULL, ok);
+                if (!ok) break;
+                ns++;
+                tc_fence_after();
+                float s[kKeys];
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 32) tmem_ld32(ts + c, *reinterpret_cast<int(*)[32]>(&s[c]));
+                tmem_wait_ld();
+                if (neg) {
+#pragma unroll
+                    for (int c = 0; c < kKeys; c++) s[c] = -s[c];
+                }
+                if (edge) {
+                    const int base = g.kbeg + j * kKeys, hi = pos - base, lo = a.window ? pos - a.window + 1 - base : -1;
+#pragma unroll
+                    for (int c = 0; c < kKeys; c++)
+                        if (c > hi || c < lo) s[c] = -INFINITY;
+                }
+                float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int c = 4; c < kKeys; c++) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
+                const bool up = mt > m + 8.0f;
+                if (__any_sync(FULL, up)) {
+                    const float f = !up ? 1.0f : (m == -INFINITY ? 0.0f : ex2(m - mt));
+                    if (up) m = mt;
+                    l *= f;
+                    if (j > 0) {
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(to + c, *reinterpret_cast<int(*)[32]>(o));
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st32(to + c, o);
                         }
                     }
-                    if (any) atomicOr(odd_values, 1u);
-                    fence_async_smem();
                 }
+                const float minus = m == -INFINITY ? 0.0f : -m;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 64) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int e = 0; e < 64; e += 2) {
+                        const float p0 = ex2(fmaf(s[c + e], scale2, minus)), p1 = ex2(fmaf(s[c + e + 1], scale2, minus));
+                        sum[e & 2] += p0;
+                        sum[(e & 2) + 1] += p1;
+                        pk[e / 2] = Elem<T>::pack(p0, p1);
+                    }
+                    // (S and P share columns: every S of the row is in registers by now)
+                    tmem_st32(ts + c / 2, pk);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_p + 16 * i + c / 8);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             }
-            ok = ok && mbar_wait(b_s + 8 * i, j & 1, abort, a.flags, kDefaultWaitNs);
+            if (n > 0) {
+                ok = ok && mbar_wait(b_o + 8 * i, no & 1, abort, a.flags, limit);
+                no++;
+            }
             ok = __all_sync(FULL, ok);
             if (!ok) break;
             tc_fence_after();
-            float s[kKeys];
-#pragma unroll
-            for (int c = 0; c < kKeys; c += 32) tmem_ld32(ts + c, *reinterpret_cast<int(*)[32]>(&s[c]));
-            tmem_wait_ld();
-            if (neg) {
-#pragma unroll
-                for (int c = 0; c < kKeys; c++) s[c] = -s[c];
-            }
-            if (edge) {
-                const int base = kbeg + j * kKeys, hi = pos - base, lo = a.window ? pos - a.window + 1 - base : -1;
-#pragma unroll
-                for (int c = 0; c < kKeys; c++)
-                    if (c > hi || c < lo) s[c] = -INFINITY;
-            }
-            float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-            for (int c = 4; c < kKeys; c++) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
-            const bool up = mt > m + 8.0f;
-            if (__any_sync(FULL, up)) {
-                const float f = !up ? 1.0f : (m == -INFINITY ? 0.0f : ex2(m - mt));
-                if (up) m = mt;
-                l *= f;
-                if (j > 0) {
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(to + c, *reinterpret_cast<int(*)[32]>(o));
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st32(to + c, o);
-                    }
-                }
-            }
-            const float minus = m == -INFINITY ? 0.0f : -m;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int c = 0; c < kKeys; c += 64) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int e = 0; e < 64; e += 2) {
-                    const float p0 = ex2(fmaf(s[c + e], scale2, minus)), p1 = ex2(fmaf(s[c + e + 1], scale2, minus));
-                    sum[e & 2] += p0;
-                    sum[(e & 2) + 1] += p1;
-                    pk[e / 2] = Elem<T>::pack(p0, p1);
-                }
-                tmem_st32(ts + c / 2, pk);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_p + 8 * i);
-        }
-        if (n > 0) ok = ok && mbar_wait(b_o + 8 * i, 0, abort, a.flags, kDefaultWaitNs);
-        ok = __all_sync(FULL, ok);
-        tc_fence_after();
-        const bool fix = ok && n > 0 && *(volatile uint32_t *)odd_values != 0;
-        const float inv = l > 0.0f || l != l ? __fdiv_rn(1.0f, l) : 0.0f;
-        const int64_t row = (int64_t)(q0 + tok) * a.heads + kvh * p.G + h;
-        if (ok) {
+            const bool fix = n > 0 && *(volatile uint32_t *)(odd_values + u % kItems) != 0;
+            const float inv = l > 0.0f || l != l ? __fdiv_rn(1.0f, l) : 0.0f;
+            const int64_t row = (int64_t)(w.q0 + tok) * a.heads + w.kvh * p.G + h;
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
                 float o[32];
@@ -455,10 +645,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     // the values that were set to 0 and that this row does see
                     const int from = max(a.window ? pos - a.window + 1 : 0, 0);
                     for (int j = 0; j < n; j++) {
-                        if (!masked(j)) continue;
-                        const int s0 = max(kbeg + j * kKeys, from), s1 = min(kbeg + (j + 1) * kKeys, pos + 1);
+                        if (!g.masked(w, a.window, j)) continue;
+                        const int s0 = max(g.kbeg + j * kKeys, from), s1 = min(g.kbeg + (j + 1) * kKeys, pos + 1);
                         for (int key = s0; key < s1; key++) {
-                            const T *v = (const T *)a.v + (int64_t)(k0 + key) * a.v_stride + (int64_t)kvh * D + c;
+                            const T *v = (const T *)a.v + (int64_t)(w.k0 + key) * a.v_stride + (int64_t)w.kvh * D + c;
 #pragma unroll
                             for (int e = 0; e < 32; e++) {
                                 const float f = (float)v[e];
@@ -478,7 +668,11 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 }
             }
             if (valid && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            tc_fence_before();   // O is read before the next item's first product writes it (ordered by P's barrier)
         }
+        t0 += 2 * n;
+        __syncwarp();
+        if (lane == 0) drop_item(u);
       }
     }
     tc_fence_before();
