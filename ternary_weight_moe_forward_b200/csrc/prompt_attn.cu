@@ -51,7 +51,7 @@ namespace {
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 // three warpgroups: two of softmax rows, one of which two warps work; the
-// launch's 384 x 168 registers are shared out as 2 x 128 x 208 + 128 x 88
+// launch's 384 x 168 registers are shared out as 2 x 128 x 216 + 128 x 72
 constexpr int kThreads = 384;
 constexpr int kKeys = 128;   // keys of a tile
 
@@ -77,6 +77,33 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// the largest of three
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // tcgen05 kind::f16: bf16 or fp16 operands, fp32 accumulator, M = 128; B either
 // K-major (keys as rows of K) or MN-major (V: its rows are the K dimension)
 __device__ __forceinline__ uint32_t idesc_f16(bool bf16, int n, bool b_mn)
@@ -579,10 +606,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     for (int c = 0; c < kKeys; c++)
                         if (c > hi || c < lo) s[c] = -INFINITY;
                 }
-                float mx[4] = {s[0], s[1], s[2], s[3]};
+                float mx[4];
 #pragma unroll
-                for (int c = 4; c < kKeys; c++) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
+                for (int c = 0; c < 4; c++) mx[c] = max3(s[3 * c], s[3 * c + 1], s[3 * c + 2]);
+#pragma unroll
+                for (int c = 12; c < kKeys; c += 2) mx[(c / 2) & 3] = max3(mx[(c / 2) & 3], s[c], s[c + 1]);
+                const float mt = max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * scale2;
                 const bool up = mt > m + 8.0f;
                 if (__any_sync(FULL, up)) {
                     const float f = !up ? 1.0f : (m == -INFINITY ? 0.0f : ex2(m - mt));
@@ -601,15 +630,19 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     }
                 }
                 const float minus = m == -INFINITY ? 0.0f : -m;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const uint64_t scale_2 = pair(scale2, scale2), minus_2 = pair(minus, minus);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int c = 0; c < kKeys; c += 64) {
                     uint32_t pk[32];
 #pragma unroll
                     for (int e = 0; e < 64; e += 2) {
-                        const float p0 = ex2(fmaf(s[c + e], scale2, minus)), p1 = ex2(fmaf(s[c + e + 1], scale2, minus));
-                        sum[e & 2] += p0;
-                        sum[(e & 2) + 1] += p1;
+                        const uint64_t x = fma2(pair(s[c + e], s[c + e + 1]), scale_2, minus_2);
+                        float p0, p1;
+                        unpair(x, p0, p1);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        sum[(e / 2) & 1] = add2(sum[(e / 2) & 1], pair(p0, p1));
                         pk[e / 2] = Elem<T>::pack(p0, p1);
                     }
                     // (S and P share columns: every S of the row is in registers by now)
@@ -619,7 +652,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     __syncwarp();
                     if (lane == 0) mbar_arrive(b_p + 16 * i + c / 8);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                float s0, s1;
+                unpair(add2(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
             }
             if (n > 0) {
                 ok = ok && mbar_wait(b_o + 8 * i, no & 1, abort, a.flags, limit);
@@ -628,6 +663,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             ok = __all_sync(FULL, ok);
             if (!ok) break;
             tc_fence_after();
+            const bool none = l == 0.0f;    // the row sees no key
             const bool fix = n > 0 && *(volatile uint32_t *)(odd_values + u % kItems) != 0;
             const float inv = l > 0.0f || l != l ? __fdiv_rn(1.0f, l) : 0.0f;
             const int64_t row = (int64_t)(w.q0 + tok) * a.heads + w.kvh * p.G + h;
@@ -662,12 +698,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     for (int e = 0; e < 32; e += 8) {
                         float y[8];
 #pragma unroll
-                        for (int z = 0; z < 8; z++) y[z] = l == 0.0f ? 0.0f : o[e + z] * inv;
+                        for (int z = 0; z < 8; z++) y[z] = none ? 0.0f : o[e + z] * inv;
                         *reinterpret_cast<uint4 *>((T *)a.out + row * D + c + e) = pack8<T>(y);
                     }
                 }
             }
-            if (valid && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            if (valid && a.lse) a.lse[row] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             tc_fence_before();   // O is read before the next item's first product writes it (ordered by P's barrier)
         }
         t0 += 2 * n;
