@@ -1,12 +1,24 @@
 // Int8 linear layer: rows quantised to int8 (absmax, one scale per token),
 // times int8 weights with one scale per output channel.  C ABI:
 // include/maple_attn.h.
+//
+// The sums are integers (exact), so nothing depends on how K is cut or ordered,
+// and every path gives the same bits.  Two paths, by the number of tokens:
+//   T <= 16   linear_rows_kernel: the weights are streamed once through
+//             warp-level int8 matrix instructions by all SMs, the tokens are
+//             quantised in the same kernel;
+//   T > 16    quantise_rows_kernel, then linear_gemm_kernel on tcgen05
+//             (kind::i8).  Up to 128 tokens the weights are the 128-row
+//             operand and all tokens one N tile (the weights are read once);
+//             above, the tokens are.
 #include <stdint.h>
+#include <string.h>
 
 #include "../../include/maple_attn.h"
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 using namespace maple;
 
@@ -21,6 +33,7 @@ __global__ void __launch_bounds__(256) quantise_rows_kernel(const uint16_t *x, i
 {
     const int lane = threadIdx.x & 31;
     const int64_t t = blockIdx.x * 8ll + (threadIdx.x >> 5);
+    asm volatile("griddepcontrol.launch_dependents;");
     if (t >= T) return;
     const uint4 *xr = reinterpret_cast<const uint4 *>(x + t * stride);
     float amax = 0.0f;
@@ -57,6 +70,7 @@ __global__ void __launch_bounds__(128) norm_quantise_rows_kernel(const float *x,
     extern __shared__ __align__(16) uint16_t rows[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = blockIdx.x * (int64_t)(blockDim.x >> 5) + warp;
+    asm volatile("griddepcontrol.launch_dependents;");
     if (t >= T) return;
     uint16_t *row = rows + (size_t)warp * K;
     rmsnorm_token_warp(x + t * stride, K, row);
@@ -97,22 +111,455 @@ struct LinearOut {
     }
 };
 
-// One thread per output
-__global__ void __launch_bounds__(256) linear_dp4a_kernel(const int8_t *q, const float *s, const int8_t *w, int64_t T, int K,
-                                                          LinearOut o)
+// ---------------------------------------------------------------------------
+// T <= 16.  A CTA takes 16 output channels at a time (m16n8k32, the weights as
+// the 16-row operand, tokens as columns), its 16 warps sharing K in pieces of 64
+// bytes: lane (g, t) reads 16 contiguous bytes of rows g and g + 8, and since the
+// order of the sum does not matter these are its fragments of two instructions,
+// against the same 16 bytes of token g's codes.  The weights go from memory to
+// registers in 16-byte loads, the next channels' before this one's sums are
+// joined.  Bound by HBM for a large N, by latency for one projection.
+// ---------------------------------------------------------------------------
+constexpr int kRowWarps = 16, kRowUnits = 2;   // warps of a CTA; 64-byte pieces of K in flight per warp
+
+__host__ __device__ __forceinline__ int row_pitch(int K)   // bytes of a token's codes: an odd multiple of 64 (no bank conflicts)
 {
-    const int64_t n = blockIdx.x * 32ll + (threadIdx.x & 31), t = blockIdx.y * 8ll + (threadIdx.x >> 5);
-    if (n >= o.N || t >= T) return;
-    const uint4 *a = reinterpret_cast<const uint4 *>(q + t * K), *b = reinterpret_cast<const uint4 *>(w + n * K);
-    int acc = 0;
-    for (int c = 0; c < K / 16; c++) {
-        const uint4 u = a[c], v = b[c];
-        acc = __dp4a((int)u.x, (int)v.x, acc);
-        acc = __dp4a((int)u.y, (int)v.y, acc);
-        acc = __dp4a((int)u.z, (int)v.z, acc);
-        acc = __dp4a((int)u.w, (int)v.w, acc);
+    const int u = (K + 63) / 64;
+    return 64 * (u | 1);
+}
+
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT: column tiles of 8 tokens
+template <int NT>
+__global__ void __launch_bounds__(kRowWarps * 32, 2)
+linear_rows_kernel(const uint16_t *x, int64_t x_stride, int T, int K, const int8_t *w, LinearOut o)
+{
+    extern __shared__ __align__(16) uint8_t codes[];        // [8 NT][pitch], then [2][16 warps][NT][32 lanes] int4
+    __shared__ float s_scale[8 * NT], s_part[kRowWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int pitch = row_pitch(K), units = (K + 63) / 64;
+    int4 *red = (int4 *)(codes + 8 * NT * pitch);
+    const int64_t tiles = (o.N + 15) / 16;
+
+    uint4 wa[kRowUnits], wb[kRowUnits];
+    auto fetch = [&](int64_t tile, int u0) {      // the warp's pieces u0, u0 + 16, ... of a tile's rows
+#pragma unroll
+        for (int i = 0; i < kRowUnits; i++) {
+            const int64_t r = tile * 16 + g;
+            const int k = 64 * (u0 + kRowWarps * i) + 16 * t;
+            const bool in = k < K;
+            wa[i] = in && r < o.N ? ld_stream_v4(w + r * K + k) : make_uint4(0, 0, 0, 0);
+            wb[i] = in && r + 8 < o.N ? ld_stream_v4(w + (r + 8) * K + k) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    if ((int64_t)blockIdx.x < tiles) fetch(blockIdx.x, warp);   // in flight while the tokens are quantised
+
+    // ---- the tokens' codes, two per round (eight warps each); rows beyond T are 0
+    for (int r0 = 0; r0 < 8 * NT; r0 += 2) {
+        const int r = r0 + (warp >> 3), tid = threadIdx.x & 255;
+        uint8_t *row = codes + r * pitch;
+        if (r0 >= T) {   // (T is the same for all threads)
+            for (int c = tid; c < pitch / 16; c += 256) reinterpret_cast<uint4 *>(row)[c] = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        const uint4 *xr = reinterpret_cast<const uint4 *>(x + (int64_t)min(r, T - 1) * x_stride);
+        float amax = 0.0f;
+        for (int c = tid; c < K / 8; c += 256) {
+            const uint4 v = __ldg(xr + c);
+            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int m = 0; m < 4; m++)
+                amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(q[m] & 0xffffu)), fabsf(bf16_bits_to_f32(q[m] >> 16))));
+        }
+        amax = warp_max(amax);
+        __syncthreads();
+        if (lane == 0) s_part[warp] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; i++) amax = fmaxf(amax, s_part[(warp & 8) + i]);
+        if (r >= T) amax = 0.0f;
+        const float inv = amax > 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;
+        for (int c = tid; c < pitch / 8; c += 256) {
+            uint32_t pk[2] = {0u, 0u};
+            if (c < K / 8 && amax > 0.0f) {
+                const uint4 v = __ldg(xr + c);
+                const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int m = 0; m < 8; m++) {
+                    const uint32_t bits = (m & 1) ? (q[m >> 1] >> 16) : (q[m >> 1] & 0xffffu);
+                    pk[m >> 2] |= (uint32_t)(quant_code(bf16_bits_to_f32(bits), inv) & 0xff) << (8 * (m & 3));
+                }
+            }
+            reinterpret_cast<uint2 *>(row)[c] = make_uint2(pk[0], pk[1]);
+        }
+        if (tid == 0) s_scale[r] = amax > 0.0f ? __fdiv_rn(amax, 127.0f) : 0.0f;
     }
-    o.store(t, n, acc, s[t]);
+    __syncthreads();
+
+    int buf = 0;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+        int c[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; j++) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0;
+        for (int u0 = warp; u0 < units; u0 += kRowWarps * kRowUnits) {
+            uint4 a[kRowUnits], b[kRowUnits];
+#pragma unroll
+            for (int i = 0; i < kRowUnits; i++) {
+                a[i] = wa[i];
+                b[i] = wb[i];
+            }
+            // the next pieces: of this tile, or the first of the CTA's next tile
+            const int next = u0 + kRowWarps * kRowUnits;
+            if (next < units) fetch(tile, next);
+            else if (tile + gridDim.x < tiles) fetch(tile + gridDim.x, warp);
+#pragma unroll
+            for (int i = 0; i < kRowUnits; i++) {
+                const int u = u0 + kRowWarps * i;
+                if (u >= units) break;
+#pragma unroll
+                for (int j = 0; j < NT; j++) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(codes + (8 * j + g) * pitch + 64 * u + 16 * t);
+                    mma_s8(c[j], a[i].x, b[i].x, a[i].y, b[i].y, q.x, q.y);
+                    mma_s8(c[j], a[i].z, b[i].z, a[i].w, b[i].w, q.z, q.w);
+                }
+            }
+        }
+        if (warp >= units && tile + gridDim.x < tiles) fetch(tile + gridDim.x, warp);   // (a warp without a piece of K: zeros)
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+            red[((buf * kRowWarps + warp) * NT + j) * 32 + lane] = make_int4(c[j][0], c[j][1], c[j][2], c[j][3]);
+        __syncthreads();
+        // output (token, channel): lane 4 (channel % 8) + token % 8 / 2, word 2 (channel / 8) + token % 2
+        for (int i = threadIdx.x; i < 16 * T; i += kRowWarps * 32) {
+            const int tok = i >> 4, ch = i & 15;
+            const int *src = (const int *)red + (((buf * kRowWarps) * NT + (tok >> 3)) * 32 + 4 * (ch & 7) + ((tok & 7) >> 1)) * 4 +
+                             2 * (ch >> 3) + (tok & 1);
+            int acc = 0;
+#pragma unroll
+            for (int v = 0; v < kRowWarps; v++) acc += src[v * NT * 128];
+            if (tile * 16 + ch < o.N) o.store(tok, tile * 16 + ch, acc, s_scale[tok]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// T > 16.  D[128 rows of A][bn rows of B], both operands K-major int8 tiles of
+// 128 bytes of K by TMA with the 128-byte swizzle, int32 accumulators in tensor
+// memory, two of them, so that the epilogue of a tile runs under the next one's
+// products.  SWAP: A is the weights and B the tokens (T <= 128), else the other
+// way round.  Warp 0 loads, warp 1 issues the products (the whole warp with the
+// same values in every lane and one lane issuing: the operands have to be in
+// uniform registers), warps 4-11 scale and store.  CTAs take tiles round robin.
+// ---------------------------------------------------------------------------
+constexpr int kGemmThreads = 384, kGemmBK = 128;
+
+struct GemmArgs {
+    LinearOut o;
+    const float *s;
+    int64_t T;
+    int K, bn, stages;
+    int64_t tiles_a, tiles_b;
+    unsigned *flag;
+};
+
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ void mma_i8_plain(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+template <bool SWAP>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+linear_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map, const GemmArgs p)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (smem_addr(smem) & 1023u) {   // the swizzled tiles need 1024-byte alignment
+        if (threadIdx.x == 0) set_flag(p.flag, MAPLE_DEVFLAG_TIMEOUT);
+        return;
+    }
+    const int S = p.stages, bn = p.bn;
+    const uint32_t stage_bytes = (128 + bn) * kGemmBK;
+    uint64_t *bars = (uint64_t *)(smem + S * stage_bytes);
+    const uint32_t b_full = smem_addr(bars), b_empty = b_full + 8 * S, b_acc = b_empty + 8 * S, b_free = b_acc + 16, b_drain = b_free + 16;
+    uint32_t *tmem_holder = (uint32_t *)(bars + 2 * S + 5);
+    volatile uint32_t *abort = tmem_holder + 1;
+    const uint64_t limit = kDefaultWaitNs;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; i++) {
+            mbar_init(b_full + 8 * i, 1);
+            mbar_init(b_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(b_acc + 8 * i, 1);
+            mbar_init(b_free + 8 * i, 8);
+        }
+        mbar_init(b_drain, 1);
+        *abort = 0u;
+        fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc(smem_addr(tmem_holder), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    const int KS = (p.K + kGemmBK - 1) / kGemmBK;      // (columns beyond K arrive as zeros)
+    const int64_t tiles = p.tiles_a * p.tiles_b;
+
+    if (warp == 0) {
+        // ---------------- loads
+        if (lane == 0) {
+            uint32_t it = 0, wrap = 0;   // stage, times round
+            int s = 0;
+            bool ok = true, waited = false;
+            for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+                const int64_t ta = tile / p.tiles_b, tb = tile - ta * p.tiles_b;
+                for (int k = 0; k < KS; k++, it++) {
+                    if (!(ok = mbar_wait(b_empty + 8 * s, (wrap & 1) ^ 1, abort, p.flag, limit))) break;
+                    const uint32_t dst = smem_addr(smem) + s * stage_bytes, bar = b_full + 8 * s;
+                    mbar_expect_tx(bar, stage_bytes);
+                    if (SWAP) {
+                        // the weights do not wait for the kernel that quantises the tokens
+                        tma_load_2d(dst, &a_map, k * kGemmBK, (int)(ta * 128), bar);
+                        if (!waited && (it + 1 == (uint32_t)S || (tile + gridDim.x >= tiles && k + 1 == KS))) {
+                            asm volatile("griddepcontrol.wait;" ::: "memory");
+                            waited = true;
+                            for (int q = 0; q <= s; q++) {   // the token tiles of the stages filled so far
+                                const int64_t qt = blockIdx.x + (int64_t)(q / KS) * gridDim.x;
+                                tma_load_2d(smem_addr(smem) + q * stage_bytes + 128 * kGemmBK, &b_map, (q % KS) * kGemmBK,
+                                            (int)((qt % p.tiles_b) * bn), b_full + 8 * q);
+                            }
+                        } else if (waited) {
+                            tma_load_2d(dst + 128 * kGemmBK, &b_map, k * kGemmBK, (int)(tb * bn), bar);
+                        }
+                    } else {
+                        if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+                        waited = true;
+                        tma_load_2d(dst, &a_map, k * kGemmBK, (int)(ta * 128), bar);
+                        tma_load_2d(dst + 128 * kGemmBK, &b_map, k * kGemmBK, (int)(tb * bn), bar);
+                    }
+                    if (++s == S) {
+                        s = 0;
+                        wrap++;
+                    }
+                }
+            }
+            if (!ok) {   // drain the copies in flight: each arrives or runs out of time
+                for (int q = 0; q < S; q++) {
+                    const uint64_t c0 = global_ns();
+                    while (global_ns() - c0 < 20000000ull && !(mbar_test(b_full + 8 * q, 0) && mbar_test(b_full + 8 * q, 1))) {
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- products
+        const bool leader = elect_one();
+        const uint32_t tm = __shfl_sync(FULL, tmem, 0), idesc = idesc_i8(bn);
+        const uint64_t d0 = desc_sw128(smem_addr(smem));
+        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(FULL, mbar_wait(bar, parity, abort, p.flag, limit)); };
+        uint32_t wrap = 0, n = 0;
+        int s = 0;
+        bool ok = true;
+        for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, n++) {
+            const uint32_t d = tm + 256 * (n & 1);
+            if (!(ok = wait(b_free + 8 * (n & 1), ((n >> 1) & 1) ^ 1))) break;
+            for (int k = 0; k < KS; k++) {
+                if (!(ok = wait(b_full + 8 * s, wrap & 1))) break;
+                tc_fence_after();
+                const uint64_t da = d0 + (uint64_t)(s * (stage_bytes / 16)), db = da + 128 * kGemmBK / 16;
+                if (leader) {
+#pragma unroll
+                    for (int q = 0; q < kGemmBK / 32; q++) mma_i8_plain(d, da + 2 * q, db + 2 * q, idesc, k > 0 || q > 0);
+                    mma_commit(b_empty + 8 * s);
+                    if (k + 1 == KS) mma_commit(b_acc + 8 * (n & 1));
+                }
+                __syncwarp();
+                if (++s == S) {
+                    s = 0;
+                    wrap++;
+                }
+            }
+        }
+        if (leader) mma_commit(b_drain);   // every issued MMA has finished before tensor memory is released
+        __syncwarp();
+        const uint64_t c0 = global_ns();
+        while (!mbar_test(b_drain, 0) && global_ns() - c0 < limit) {
+        }
+    } else if (warp >= 4) {
+        // ---------------- epilogue: lane quarter warp % 4, every other 32 columns
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // (the scales)
+        const int q = warp & 3, half = (warp - 4) >> 2, r = 32 * q + lane;
+        const LinearOut &o = p.o;
+        uint32_t n = 0;
+        for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, n++) {
+            const int64_t ta = tile / p.tiles_b, tb = tile - ta * p.tiles_b;
+            const int64_t row = ta * 128 + r;
+            const bool in = row < (SWAP ? o.N : p.T);
+            const float fr = in ? (SWAP ? __ldg(o.alpha + row) : __ldg(p.s + row)) : 0.0f;
+            if (!__all_sync(FULL, mbar_wait(b_acc + 8 * (n & 1), (n >> 1) & 1, abort, p.flag, limit))) break;
+            tc_fence_after();
+            const uint32_t src = tmem + 256 * (n & 1) + ((uint32_t)(32 * q) << 16);
+            for (int c0 = 32 * half; c0 < bn; c0 += 64) {
+                int acc[32];
+                tmem_ld32(src + c0, acc);
+                tmem_wait_ld();
+                const int64_t col = tb * bn + c0;
+                if (SWAP) {
+                    // lane = channel, columns = tokens: a warp writes 32 neighbours of a token's row
+#pragma unroll
+                    for (int c = 0; c < 32; c++)
+                        if (in && col + c < p.T) o.store(col + c, row, acc[c], __ldg(p.s + col + c));
+                } else if (in) {
+                    // lane = token, columns = channels
+                    float v[32];
+                    if (col + 32 <= o.N && (o.N & 7) == 0) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 al = __ldg(reinterpret_cast<const float4 *>(o.alpha + col + c));
+                            v[c] = __fmul_rn((float)acc[c], __fmul_rn(al.x, fr));
+                            v[c + 1] = __fmul_rn((float)acc[c + 1], __fmul_rn(al.y, fr));
+                            v[c + 2] = __fmul_rn((float)acc[c + 2], __fmul_rn(al.z, fr));
+                            v[c + 3] = __fmul_rn((float)acc[c + 3], __fmul_rn(al.w, fr));
+                        }
+                        if (o.bias) {
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4) {
+                                const float4 bi = __ldg(reinterpret_cast<const float4 *>(o.bias + col + c));
+                                v[c] = __fadd_rn(v[c], bi.x);
+                                v[c + 1] = __fadd_rn(v[c + 1], bi.y);
+                                v[c + 2] = __fadd_rn(v[c + 2], bi.z);
+                                v[c + 3] = __fadd_rn(v[c + 3], bi.w);
+                            }
+                        }
+                        if (o.resid) {
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4) {
+                                const float4 re = *reinterpret_cast<const float4 *>(o.resid + row * o.N + col + c);
+                                v[c] = __fadd_rn(re.x, v[c]);
+                                v[c + 1] = __fadd_rn(re.y, v[c + 1]);
+                                v[c + 2] = __fadd_rn(re.z, v[c + 2]);
+                                v[c + 3] = __fadd_rn(re.w, v[c + 3]);
+                            }
+                        }
+                        if (o.y_bf16) {
+                            uint4 *dst = reinterpret_cast<uint4 *>((uint16_t *)o.y + row * o.N + col);
+#pragma unroll
+                            for (int c = 0; c < 32; c += 8) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int z = 0; z < 4; z++) {
+                                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[c + 2 * z], v[c + 2 * z + 1]);
+                                    w[z] = *reinterpret_cast<const uint32_t *>(&b);
+                                }
+                                dst[c / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        } else {
+                            float4 *dst = reinterpret_cast<float4 *>((float *)o.y + row * o.N + col);
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4) dst[c / 4] = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 32; c++)
+                            if (col + c < o.N) o.store(row, col + c, acc[c], fr);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_free + 8 * (n & 1));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+typedef CUresult (*encode_fn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// int8 [rows][K], boxes of `box` rows x 128 bytes, 128-byte swizzle
+int row_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int box)
+{
+    static encode_fn encode = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return (encode_fn)fn;
+    }();
+    if (!encode) return MAPLE_ERR_CUDA;
+    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)K};
+    cuuint32_t b[2] = {kGemmBK, (cuuint32_t)box}, estr[2] = {1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, b, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MAPLE_OK : MAPLE_ERR_CUDA;
+}
+
+constexpr int kRowTokens = 16;      // most tokens of linear_rows_kernel
+constexpr int kRowCodes = 98304;    // and most bytes of their codes in shared memory (two CTAs on an SM)
+
+int rows_smem(int64_t T, int K)
+{
+    const int NT = T <= 8 ? 1 : 2;
+    return 8 * NT * row_pitch(K) + 2 * kRowWarps * NT * 512;
+}
+bool rows_path(int64_t T, int K, bool normalise) { return T <= kRowTokens && !normalise && rows_smem(T, K) <= kRowCodes; }
+
+template <int NT>
+int launch_rows(const maple_attn_linear_args &a, const LinearOut &o, cudaStream_t st)
+{
+    const int smem = rows_smem(a.T, (int)a.K);
+    if (smem > 49152 && cudaFuncSetAttribute(linear_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowCodes) != cudaSuccess) {
+        cudaGetLastError();
+        return MAPLE_ERR_CUDA;
+    }
+    const int64_t tiles = (a.N + 15) / 16;
+    linear_rows_kernel<NT><<<(unsigned)(tiles < 2 * 148 ? tiles : 2 * 148), kRowWarps * 32, smem, st>>>(
+        (const uint16_t *)a.x, a.x_stride, (int)a.T, (int)a.K, a.w, o);
+    return cudaGetLastError() == cudaSuccess ? MAPLE_OK : MAPLE_ERR_CUDA;
+}
+
+// Tile width of the T > 128 form: rounds of the 148 SMs times the width (plus
+// what a tile costs whatever its width), the least over 64 .. 256
+int pick_bn(int64_t T, int64_t N)
+{
+    const int64_t ta = (T + 127) / 128;
+    int best = 64;
+    int64_t cost = -1;
+    for (int bn = 64; bn <= 256; bn += 32) {
+        const int64_t rounds = (ta * ((N + bn - 1) / bn) + 147) / 148;
+        const int64_t c = rounds * (bn < 128 ? 64 + bn / 2 + 16 : bn + 16);   // (below 128 the 128-row operand's reads set the pace)
+        if (cost < 0 || c < cost || (c == cost && bn > best)) {
+            cost = c;
+            best = bn;
+        }
+    }
+    return best;
 }
 
 int64_t round256(int64_t v) { return (v + 255) & ~255ll; }
@@ -131,7 +578,7 @@ extern "C" int64_t maple_attn_linear_workspace(int64_t T, int64_t K, int64_t N)
 {
     const int rc = check_sizes(T, K, N);
     if (rc) return rc;
-    return round256(T * K) + round256(T * 4);
+    return round256(T * K) + round256(T * 4);   // (the largest need: few tokens are quantised in shared memory)
 }
 
 extern "C" int maple_attn_linear(const maple_attn_linear_args *args, maple_stream_t stream)
@@ -149,11 +596,37 @@ extern "C" int maple_attn_linear(const maple_attn_linear_args *args, maple_strea
         if (!aligned16(p)) return MAPLE_ERR_INVALID_ARG;
     if (a.x_stride % 8) return MAPLE_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
+    const int K = (int)a.K;
+    const LinearOut o{a.alpha, a.bias, a.resid, a.y, a.N, a.y_dtype == MAPLE_BF16};
+    if (rows_path(a.T, K, a.normalise)) return a.T <= 8 ? launch_rows<1>(a, o, st) : launch_rows<2>(a, o, st);
+
     int8_t *q = (int8_t *)a.workspace;
     float *s = (float *)((char *)a.workspace + round256(a.T * a.K));
-    const int K = (int)a.K;
+    const bool swap = a.T <= 128;
+    GemmArgs p;
+    memset(&p, 0, sizeof p);
+    p.o = o;
+    p.s = s;
+    p.T = a.T;
+    p.K = K;
+    p.bn = swap ? (int)((a.T + 15) / 16 * 16) : pick_bn(a.T, a.N);
+    p.flag = a.flags;
+    p.tiles_a = ((swap ? a.N : a.T) + 127) / 128;
+    p.tiles_b = ((swap ? a.T : a.N) + p.bn - 1) / p.bn;
+    CUtensorMap qm, wm;
+    int rc = row_map(&qm, q, a.T, K, swap ? p.bn : 128);
+    if (!rc) rc = row_map(&wm, a.w, a.N, K, swap ? 128 : p.bn);
+    if (rc) return rc;
+    const int stage = (128 + p.bn) * kGemmBK;
+    p.stages = 212992 / stage < 8 ? 212992 / stage : 8;
+    const int smem = p.stages * stage + 256;
+    auto kernel = swap ? linear_gemm_kernel<true> : linear_gemm_kernel<false>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 216 * 1024) != cudaSuccess) {
+        cudaGetLastError();
+        return MAPLE_ERR_CUDA;
+    }
     if (a.normalise) {
-        const int warps = K <= 4096 ? 4 : 1;   // (K bf16 values of shared memory a warp: 32 KB at most below the opt-in limit)
+        const int warps = K <= 4096 ? 4 : 1;   // (K bf16 values of shared memory a warp)
         if ((size_t)warps * K * 2 > 49152 &&
             cudaFuncSetAttribute(norm_quantise_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536) != cudaSuccess) {
             cudaGetLastError();
@@ -164,8 +637,21 @@ extern "C" int maple_attn_linear(const maple_attn_linear_args *args, maple_strea
     } else {
         quantise_rows_kernel<<<(unsigned)((a.T + 7) / 8), 256, 0, st>>>((const uint16_t *)a.x, a.x_stride, a.T, K, q, s);
     }
-    const LinearOut o{a.alpha, a.bias, a.resid, a.y, a.N, a.y_dtype == MAPLE_BF16};
-    if ((a.T + 7) / 8 > 65535) return MAPLE_ERR_UNSUPPORTED_SHAPE;
-    linear_dp4a_kernel<<<dim3((unsigned)((a.N + 31) / 32), (unsigned)((a.T + 7) / 8)), 256, 0, st>>>(q, s, a.w, a.T, K, o);
+    cudaLaunchConfig_t lc;
+    memset(&lc, 0, sizeof lc);
+    const int64_t tiles = p.tiles_a * p.tiles_b;
+    lc.gridDim = dim3((unsigned)(tiles < 148 ? tiles : 148));
+    lc.blockDim = dim3(kGemmThreads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    if (cudaLaunchKernelEx(&lc, kernel, swap ? wm : qm, swap ? qm : wm, p) != cudaSuccess) {
+        cudaGetLastError();
+        return MAPLE_ERR_CUDA;
+    }
     return cudaGetLastError() == cudaSuccess ? MAPLE_OK : MAPLE_ERR_CUDA;
 }
