@@ -56,24 +56,22 @@ def _lib():
     return _fn
 
 
-def _need(ok, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+# The device and stream that torch has current, without building the Python objects around them: these functions are
+# called once per operator and token.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _p(t) -> int:
-    return 0 if t is None else t.data_ptr()
-
-
-def _call(name: str, args: bytes, device, stream) -> None:
+def _call(name: str, args: bytes, dev: int, stream) -> None:
     """Launch on `stream` or the device's current one, with that device current."""
-    fn = getattr(_lib(), "maple_attn_" + name)
-    here = torch.cuda.current_device()
-    if device.index != here:
-        with torch.cuda.device(device):
-            rc = fn(args, torch.cuda.current_stream().cuda_stream if stream is None else stream)
+    fn = getattr(_fn or _lib(), "maple_attn_" + name)
+    if stream is None:
+        stream = _raw_stream(dev)
+    if dev == _current_device():
+        rc = fn(args, stream)
     else:
-        rc = fn(args, torch.cuda.current_stream().cuda_stream if stream is None else stream)
+        with torch.cuda.device(dev):
+            rc = fn(args, stream)
     if rc != MAPLE_OK:
         raise MapleError(rc, "maple_attn_" + name)
 
@@ -84,24 +82,43 @@ def _size(n: int, what: str) -> int:
     return n
 
 
-def _same_device(device, *tensors) -> None:
-    _need(device.type == "cuda", "the tensors must be on a CUDA device")
-    for t in tensors:
-        _need(t is None or t.device == device, f"all tensors must be on {device}")
+def _device(first, *others) -> int:
+    """The CUDA device index that all tensors (None aside) are on."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on one device")
+    return dev
 
 
-def _check_flags(flags) -> None:
-    _need(flags is None or (flags.dtype is torch.int32 and flags.numel() == 1), "flags must be one int32")
+def _flags(t) -> int:
+    if t is None:
+        return 0
+    if t.dtype is not torch.int32 or t.numel() != 1:
+        raise ValueError("flags must be one int32")
+    return t.data_ptr()
 
 
-def _heads(t, name: str, dtype=None):
-    """A [tokens][heads][head_dim] tensor whose heads are contiguous within a token; returns its token stride."""
-    _need(t.dim() == 3, f"{name} must be [tokens][heads][head_dim]")
+def _vector(t, dtype, n: int, what: str) -> int:
+    """Address of a contiguous vector of n values (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(what)
+    return t.data_ptr()
+
+
+def _heads(t, dtype, what: str):
+    """A [tokens][heads][head_dim] tensor whose heads are contiguous within a token; returns its shape and token stride."""
+    if t.dim() != 3 or t.dtype is not dtype:
+        raise ValueError(what)
     n, h, d = t.shape
     s = t.stride()
-    _need(s[2] == 1 and (h == 1 or s[1] == d), f"{name}: a token's heads must be contiguous")
-    _need(dtype is None or t.dtype is dtype, f"{name} must be {dtype}")
-    return s[0] if n > 1 else h * d
+    if s[2] != 1 or (s[1] != d and h != 1):
+        raise ValueError(what)
+    return n, h, d, (s[0] if n > 1 else h * d)
 
 
 def kv_pages(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, device="cuda") -> torch.Tensor:
@@ -111,11 +128,13 @@ def kv_pages(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, 
 
 
 def _page_size(pages, kv_heads: int, head_dim: int) -> int:
-    _need(pages.dtype is torch.uint8 and pages.dim() == 3 and pages.is_contiguous(),
-          "pages must be a contiguous uint8 [num_pages][kv_heads][page bytes]")
-    _need(pages.shape[1] == kv_heads, f"the cache holds {pages.shape[1]} key/value heads, not {kv_heads}")
+    if pages.dtype is not torch.uint8 or pages.dim() != 3 or not pages.is_contiguous():
+        raise ValueError("pages must be a contiguous uint8 [num_pages][kv_heads][page bytes]")
+    if pages.shape[1] != kv_heads:
+        raise ValueError("the cache holds another number of key/value heads")
     n, rest = divmod(pages.shape[2] * 4, 5 * head_dim)
-    _need(rest == 0 and n in (16, 32, 64), f"pages of {pages.shape[2]} bytes do not fit head_dim {head_dim}")
+    if rest or n not in (16, 32, 64):
+        raise ValueError("the pages do not fit this head_dim")
     return n
 
 
@@ -127,28 +146,32 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias
     x bf16 [T][K] (rows may be strided), or the fp32 residual stream with `normalise` (its RMS-normed rows, rounded to
     bf16, are quantised).  weight int8 [N][K], alpha fp32 [N], bias fp32 [N], resid fp32 [T][N] (may be `out`).
     """
-    _need(x.dim() == 2 and weight.dim() == 2 and x.shape[1] == weight.shape[1], "x must be [T][K] and weight [N][K]")
+    if x.dim() != 2 or weight.dim() != 2 or x.shape[1] != weight.shape[1]:
+        raise ValueError("x must be [T][K] and weight [N][K]")
     T, K = x.shape
     N = weight.shape[0]
-    dev = x.device
-    _same_device(dev, weight, alpha, bias, resid, out, flags)
-    _need(x.dtype is (torch.float32 if normalise else torch.bfloat16), "x must be bf16, or fp32 with normalise")
-    _need(x.stride(1) == 1 or K == 1, "the rows of x must be contiguous")
-    _need(weight.dtype is torch.int8 and weight.is_contiguous(), "weight must be contiguous int8")
-    for v, name in ((alpha, "alpha"), (bias, "bias")):
-        _need(v is None or (v.dtype is torch.float32 and v.shape == (N,) and v.is_contiguous()), f"{name} must be fp32 [N]")
-    _need(resid is None or (resid.dtype is torch.float32 and resid.shape == (T, N) and resid.is_contiguous()),
-          "resid must be contiguous fp32 [T][N]")
+    dev = _device(x, weight, alpha, bias, resid, out, flags)
+    if x.dtype is not (torch.float32 if normalise else torch.bfloat16):
+        raise ValueError("x must be bf16, or fp32 with normalise")
+    if x.stride(1) != 1 and K != 1:
+        raise ValueError("the rows of x must be contiguous")
+    if weight.dtype is not torch.int8 or not weight.is_contiguous():
+        raise ValueError("weight must be contiguous int8")
+    if resid is not None and (resid.dtype is not torch.float32 or resid.shape != (T, N) or not resid.is_contiguous()):
+        raise ValueError("resid must be contiguous fp32 [T][N]")
     if out is None:
-        _need(out_dtype in _OUT_TYPES, "out_dtype must be bf16 or fp32")
-        out = torch.empty((T, N), dtype=out_dtype, device=dev)
-    else:
-        _need(out.dtype in _OUT_TYPES and out.shape == (T, N) and out.is_contiguous(), "out must be contiguous bf16 or fp32 [T][N]")
-    _check_flags(flags)
-    n = _size(_lib().maple_attn_linear_workspace(T, K, N), "maple_attn_linear")
-    ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    _call("linear", _LINEAR.pack(_p(x), _p(weight), _p(alpha), _p(bias), _p(resid), _p(out), _p(ws), n, _p(flags),
-                                 x.stride(0) if T > 1 else K, T, K, N, _OUT_TYPES[out.dtype], int(normalise)), dev, stream)
+        out = torch.empty((T, N), dtype=out_dtype, device=x.device)
+    elif out.shape != (T, N) or not out.is_contiguous():
+        raise ValueError("out must be contiguous [T][N]")
+    ydt = _OUT_TYPES.get(out.dtype)
+    if ydt is None:
+        raise ValueError("the output must be bf16 or fp32")
+    n = _size((_fn or _lib()).maple_attn_linear_workspace(T, K, N), "maple_attn_linear")
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    _call("linear", _LINEAR.pack(
+        x.data_ptr(), weight.data_ptr(), _vector(alpha, torch.float32, N, "alpha must be fp32 [N]"),
+        _vector(bias, torch.float32, N, "bias must be fp32 [N]"), 0 if resid is None else resid.data_ptr(), out.data_ptr(),
+        ws.data_ptr(), n, _flags(flags), x.stride(0) if T > 1 else K, T, K, N, ydt, 1 if normalise else 0), dev, stream)
     return out
 
 
@@ -163,49 +186,52 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_
     store, distinct otherwise) the rotated keys and the values are also written to the cache.
     """
     dt = q.dtype
-    _need(dt in _HEAD_TYPES, "q must be bf16 or fp16")
-    qs, ks = _heads(q, "q"), _heads(k, "k", dt)
-    T, H, d = q.shape
-    Hkv = k.shape[1]
-    dev = q.device
-    _same_device(dev, k, positions, inv_freq, q_weight, k_weight, v, pages, slots, flags)
-    _need(k.shape == (T, Hkv, d), "k must hold the same tokens and head_dim as q")
-    _need(positions.dtype is torch.int64 and positions.shape == (T,) and positions.is_contiguous(), "positions must be int64 [T]")
-    _need(inv_freq.dtype is torch.float64 and inv_freq.dim() == 1 and inv_freq.is_contiguous(), "inv_freq must be float64 [rotary_dim/2]")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        _need(w is None or (w.dtype is torch.float32 and w.shape == (d,) and w.is_contiguous()), f"{name} must be fp32 [head_dim]")
-    _need((pages is None) == (v is None) == (slots is None), "pages, v and slots go together")
-    vs = n = P = 0
+    if dt not in _HEAD_TYPES:
+        raise ValueError("q must be bf16 or fp16")
+    T, H, d, qs = _heads(q, dt, "q must be [T][heads][d], a token's heads contiguous")
+    Tk, Hkv, dk, ks = _heads(k, dt, "k must be [T][kv_heads][d] of q's type, a token's heads contiguous")
+    if Tk != T or dk != d:
+        raise ValueError("k must hold the same tokens and head_dim as q")
+    dev = _device(q, k, positions, inv_freq, q_weight, k_weight, v, pages, slots, flags)
+    vs = n = P = vp = pp = 0
     if pages is not None:
-        vs = _heads(v, "v", dt)
-        _need(v.shape == k.shape, "v must have the shape of k")
-        _need(slots.dtype is torch.int64 and slots.shape == (T,) and slots.is_contiguous(), "slots must be int64 [T]")
-        n, P = _page_size(pages, Hkv, d), pages.shape[0]
-    _check_flags(flags)
-    qo = torch.empty((T, H, d), dtype=dt, device=dev)
-    ko = torch.empty((T, Hkv, d), dtype=dt, device=dev)
-    _call("qk_norm_rope", _ROPE.pack(_p(q), _p(k), _p(v), _p(qo), _p(ko), _p(q_weight), _p(k_weight), _p(positions),
-                                     _p(inv_freq), _p(pages), _p(slots), _p(flags), qs, ks, vs, T, P, H, Hkv, d,
-                                     2 * inv_freq.shape[0], n, _HEAD_TYPES[dt], int(interleaved), eps), dev, stream)
+        if v is None or slots is None:
+            raise ValueError("pages, v and slots go together")
+        vs = _heads(v, dt, "v must be [T][kv_heads][d] of q's type, a token's heads contiguous")[3]
+        if v.shape != k.shape:
+            raise ValueError("v must have the shape of k")
+        n, P, vp, pp = _page_size(pages, Hkv, d), pages.shape[0], v.data_ptr(), pages.data_ptr()
+    elif v is not None or slots is not None:
+        raise ValueError("pages, v and slots go together")
+    qo = torch.empty((T, H, d), dtype=dt, device=q.device)
+    ko = torch.empty((T, Hkv, d), dtype=dt, device=q.device)
+    rot = inv_freq.shape[0]
+    _call("qk_norm_rope", _ROPE.pack(
+        q.data_ptr(), k.data_ptr(), vp, qo.data_ptr(), ko.data_ptr(),
+        _vector(q_weight, torch.float32, d, "q_weight must be fp32 [head_dim]"),
+        _vector(k_weight, torch.float32, d, "k_weight must be fp32 [head_dim]"),
+        _vector(positions, torch.int64, T, "positions must be int64 [T]"),
+        _vector(inv_freq, torch.float64, rot, "inv_freq must be float64 [rotary_dim/2]"), pp,
+        _vector(slots, torch.int64, T, "slots must be int64 [T]"), _flags(flags), qs, ks, vs, T, P, H, Hkv, d, 2 * rot, n,
+        _HEAD_TYPES[dt], 1 if interleaved else 0, eps), dev, stream)
     return qo, ko
 
 
 def kv_read(pages: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: torch.dtype = torch.bfloat16,
             flags: torch.Tensor | None = None, stream: int | None = None):
     """(k, v) [n][kv_heads][head_dim]: the values that the cache holds at `slots` (int64 [n]; < 0 reads as zeros)."""
-    _need(dtype in _HEAD_TYPES, "dtype must be bf16 or fp16")
-    _need(pages.dim() == 3, "pages must be [num_pages][kv_heads][page bytes]")
-    P, Hkv = pages.shape[:2]
+    if dtype not in _HEAD_TYPES:
+        raise ValueError("dtype must be bf16 or fp16")
+    if pages.dim() != 3 or slots.dim() != 1:
+        raise ValueError("pages must be [num_pages][kv_heads][page bytes] and slots [n]")
+    P, Hkv = pages.shape[0], pages.shape[1]
     page_size = _page_size(pages, Hkv, head_dim)
-    dev = pages.device
-    _same_device(dev, slots, flags)
-    _need(slots.dtype is torch.int64 and slots.dim() == 1 and slots.is_contiguous(), "slots must be int64 [n]")
-    _check_flags(flags)
+    dev = _device(pages, slots, flags)
     n = slots.shape[0]
-    k = torch.empty((n, Hkv, head_dim), dtype=dtype, device=dev)
-    v = torch.empty((n, Hkv, head_dim), dtype=dtype, device=dev)
-    _call("kv_read", _READ.pack(_p(pages), _p(slots), _p(k), _p(v), _p(flags), n, P, Hkv, head_dim, page_size,
-                                _HEAD_TYPES[dtype]), dev, stream)
+    k = torch.empty((n, Hkv, head_dim), dtype=dtype, device=pages.device)
+    v = torch.empty((n, Hkv, head_dim), dtype=dtype, device=pages.device)
+    _call("kv_read", _READ.pack(pages.data_ptr(), _vector(slots, torch.int64, n, "slots must be int64 [n]"), k.data_ptr(),
+                                v.data_ptr(), _flags(flags), n, P, Hkv, head_dim, page_size, _HEAD_TYPES[dtype]), dev, stream)
     return k, v
 
 
@@ -220,24 +246,27 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     written (`out` keeps them).
     """
     dt = q.dtype
-    _need(dt in _HEAD_TYPES, "q must be bf16 or fp16")
-    qs, ks, vs = _heads(q, "q"), _heads(k, "k", dt), _heads(v, "v", dt)
-    Tq, H, d = q.shape
-    Tk, Hkv = k.shape[:2]
-    dev = q.device
-    _same_device(dev, k, v, cu_q, cu_k, out, flags)
-    _need(k.shape == v.shape and k.shape[2] == d, "k and v must have one shape and q's head_dim")
+    if dt not in _HEAD_TYPES:
+        raise ValueError("q must be bf16 or fp16")
+    Tq, H, d, qs = _heads(q, dt, "q must be [Tq][heads][d], a token's heads contiguous")
+    Tk, Hkv, dk, ks = _heads(k, dt, "k must be [Tk][kv_heads][d] of q's type, a token's heads contiguous")
+    vs = _heads(v, dt, "v must be [Tk][kv_heads][d] of q's type, a token's heads contiguous")[3]
+    if k.shape != v.shape or dk != d:
+        raise ValueError("k and v must have one shape and q's head_dim")
+    dev = _device(q, k, v, cu_q, cu_k, out, flags)
     B = cu_q.shape[0] - 1
-    for c, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
-        _need(c.dtype is torch.int32 and c.dim() == 1 and c.shape[0] == B + 1 >= 1 and c.is_contiguous(), f"{name} must be int32 [B+1]")
-    _check_flags(flags)
+    if B < 0:
+        raise ValueError("cu_q must be int32 [B+1]")
     if out is None:
-        out = torch.empty((Tq, H, d), dtype=dt, device=dev)
-    else:
-        _need(out.dtype is dt and out.shape == (Tq, H, d) and out.is_contiguous(), "out must be contiguous, of q's type and shape")
-    lse = torch.empty((Tq, H), dtype=torch.float32, device=dev) if return_lse else None
-    _call("prompt", _PROMPT.pack(_p(q), _p(k), _p(v), _p(out), _p(lse), _p(cu_q), _p(cu_k), _p(flags), qs, ks, vs, Tq, Tk,
-                                 B, max_q, H, Hkv, d, window, _HEAD_TYPES[dt], d ** -0.5 if scale is None else scale), dev, stream)
+        out = torch.empty((Tq, H, d), dtype=dt, device=q.device)
+    elif out.dtype is not dt or out.shape != (Tq, H, d) or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's type and shape")
+    lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device) if return_lse else None
+    _call("prompt", _PROMPT.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+        _vector(cu_q, torch.int32, B + 1, "cu_q must be int32 [B+1]"), _vector(cu_k, torch.int32, B + 1, "cu_k must be int32 [B+1]"),
+        _flags(flags), qs, ks, vs, Tq, Tk, B, max_q, H, Hkv, d, window, _HEAD_TYPES[dt], d ** -0.5 if scale is None else scale),
+        dev, stream)
     return (out, lse) if return_lse else out
 
 
@@ -250,23 +279,23 @@ def cached_attention(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Te
     (the new one among them).  scale and window as in prompt_attention; an empty sequence gives a row of zeros.
     """
     dt = q.dtype
-    _need(dt in _HEAD_TYPES, "q must be bf16 or fp16")
-    qs = _heads(q, "q")
-    B, H, d = q.shape
-    dev = q.device
-    _same_device(dev, pages, block_table, lens, flags)
-    _need(pages.dim() == 3, "pages must be [num_pages][kv_heads][page bytes]")
-    P, Hkv = pages.shape[:2]
+    if dt not in _HEAD_TYPES:
+        raise ValueError("q must be bf16 or fp16")
+    B, H, d, qs = _heads(q, dt, "q must be [B][heads][d], a token's heads contiguous")
+    if pages.dim() != 3:
+        raise ValueError("pages must be [num_pages][kv_heads][page bytes]")
+    P, Hkv = pages.shape[0], pages.shape[1]
     n = _page_size(pages, Hkv, d)
-    _need(block_table.dtype is torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B and
-          (block_table.stride(1) == 1 or block_table.shape[1] <= 1), "block_table must be int32 [B][max_pages]")
-    _need(lens.dtype is torch.int32 and lens.shape == (B,) and lens.is_contiguous(), "lens must be int32 [B]")
-    _check_flags(flags)
+    dev = _device(q, pages, block_table, lens, flags)
+    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or (
+            block_table.stride(1) != 1 and block_table.shape[1] > 1):
+        raise ValueError("block_table must be int32 [B][max_pages]")
     mp = block_table.shape[1]
-    out = torch.empty((B, H, d), dtype=dt, device=dev)
-    w = _size(_lib().maple_attn_cached_workspace(B, mp, H, Hkv, d, n, window), "maple_attn_cached")
-    ws = torch.empty(w, dtype=torch.uint8, device=dev) if w else None
-    _call("cached", _CACHED.pack(_p(q), _p(out), _p(pages), _p(block_table), _p(lens), _p(ws), w, _p(flags), qs,
-                                 block_table.stride(0) if B > 1 else mp, P, B, mp, H, Hkv, d, n, window, _HEAD_TYPES[dt],
-                                 d ** -0.5 if scale is None else scale), dev, stream)
+    out = torch.empty((B, H, d), dtype=dt, device=q.device)
+    w = _size((_fn or _lib()).maple_attn_cached_workspace(B, mp, H, Hkv, d, n, window), "maple_attn_cached")
+    ws = torch.empty(w, dtype=torch.uint8, device=q.device) if w else None
+    _call("cached", _CACHED.pack(
+        q.data_ptr(), out.data_ptr(), pages.data_ptr(), block_table.data_ptr(), _vector(lens, torch.int32, B, "lens must be int32 [B]"),
+        0 if ws is None else ws.data_ptr(), w, _flags(flags), qs, block_table.stride(0) if B > 1 else mp, P, B, mp, H, Hkv, d, n, window,
+        _HEAD_TYPES[dt], d ** -0.5 if scale is None else scale), dev, stream)
     return out
