@@ -188,3 +188,4 @@ def maple_moe_destroy(handle) -> None:
 from .layer import Layer, upload_layer  # noqa: E402  (torch-side convenience)
 from .attention import (cached_attention, int8_linear, kv_pages, kv_read, prompt_attention,  # noqa: E402
                         qk_norm_rope)
+from .stack import AttentionLayer, DecoderStack  # noqa: E402

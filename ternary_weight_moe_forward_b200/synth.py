@@ -25,7 +25,7 @@ import dataclasses
 import numpy as np
 
 __all__ = [
-    "LayerShape", "CONFIGS", "layer_weights", "activations", "zipf_bias",
+    "LayerShape", "CONFIGS", "layer_weights", "activations", "zipf_bias", "attention_weights",
     "bf16_bits_to_f32", "f32_to_bf16_bits", "ternary_matrix",
 ]
 
@@ -33,6 +33,7 @@ __all__ = [
 _T_GATE, _T_UP, _T_DOWN = 1, 2, 3
 _T_AGATE, _T_AUP, _T_ADOWN = 4, 5, 6
 _T_ROUTER, _T_X, _T_BIAS, _T_RESID = 7, 8, 9, 10
+_T_QKV, _T_OUT, _T_NORM = 11, 12, 13
 
 
 @dataclasses.dataclass(frozen=True)
@@ -108,6 +109,21 @@ def layer_weights(shape: LayerShape, seed: int, layer: int = 0, zipf: float | No
         "router_bias": None if zipf is None else zipf_bias(E, zipf, seed, layer),
     }
     return w
+
+
+def attention_weights(d_model: int, heads: int, kv_heads: int, head_dim: int, seed: int, layer: int = 0) -> dict:
+    """Weights of one attention sublayer as plain arrays: int8 codes uniform in -127 .. 127, lognormal scales per output
+    channel such that a projection of unit rows has outputs near 1, head norm weights near 1."""
+    n, m = (heads + 2 * kv_heads) * head_dim, heads * head_dim
+    rq, ro, rn = _rng(seed, layer, _T_QKV), _rng(seed, layer, _T_OUT), _rng(seed, layer, _T_NORM)
+    codes = lambda r, rows, cols: r.integers(-127, 128, size=(rows, cols), dtype=np.int8)  # noqa: E731
+    alpha = lambda r, rows, cols: (np.exp(0.25 * r.standard_normal(rows)) / (73.0 * np.sqrt(cols))).astype(np.float32)  # noqa: E731
+    return {
+        "qkv": codes(rq, n, d_model), "alpha_qkv": alpha(rq, n, d_model),
+        "out": codes(ro, d_model, m), "alpha_out": alpha(ro, d_model, m),
+        "q_norm": (1.0 + 0.1 * rn.standard_normal(head_dim)).astype(np.float32),
+        "k_norm": (1.0 + 0.1 * rn.standard_normal(head_dim)).astype(np.float32),
+    }
 
 
 def layer_weights_from_args(args) -> dict:
