@@ -86,7 +86,7 @@ typedef struct {
     const float *bias;      /* [N] or NULL */
     const float *resid;     /* [T][N] fp32 or NULL */
     void *y;                /* [T][N] of y_dtype */
-    void *workspace;        /* maple_attn_linear_workspace bytes */
+    void *workspace;        /* maple_attn_linear_workspace bytes; NULL where that is 0 */
     int64_t workspace_bytes;
     uint32_t *flags;
     int64_t x_stride;       /* elements from row to row of x (a multiple of 8) */
@@ -95,7 +95,8 @@ typedef struct {
     int32_t normalise;
 } maple_attn_linear_args;
 
-int64_t maple_attn_linear_workspace(int64_t T, int64_t K, int64_t N);
+/* Bytes of workspace that a call needs (0: none), or a negative MAPLE_ERR_* code. */
+int64_t maple_attn_linear_workspace(int64_t T, int64_t K, int64_t N, int32_t normalise);
 int maple_attn_linear(const maple_attn_linear_args *args, maple_stream_t stream);
 
 /*
@@ -183,7 +184,7 @@ typedef struct {
     const uint8_t *pages;
     const int32_t *block_table;     /* [B][max_pages] (table_stride from row to row) */
     const int32_t *lens;            /* [B] */
-    void *workspace;                /* maple_attn_cached_workspace bytes */
+    void *workspace;                /* maple_attn_cached_workspace bytes; NULL where that is 0 */
     int64_t workspace_bytes;
     uint32_t *flags;
     int64_t q_stride, table_stride, num_pages;

@@ -24,7 +24,7 @@ import struct
 
 import torch
 
-from . import MAPLE_OK, MapleError, lib
+from . import MapleError, lib
 
 MAPLE_BF16, MAPLE_FP16, MAPLE_FP32 = 0, 1, 2
 
@@ -39,6 +39,8 @@ _PROMPT = struct.Struct("=8Q 5q 7i f")
 _CACHED = struct.Struct("=6Q q Q 3q 8i f 4x")
 
 _fn = None
+_calls = {}     # the entry points by name
+_UNIT = (1,)
 
 
 def _lib():
@@ -49,8 +51,9 @@ def _lib():
         for name in ("linear", "qk_norm_rope", "kv_read", "prompt", "cached"):
             f = getattr(L, "maple_attn_" + name)
             f.argtypes, f.restype = [C.c_char_p, P], C.c_int
+            _calls[name] = f
         L.maple_attn_page_bytes.argtypes, L.maple_attn_page_bytes.restype = [I32, I32], I64
-        L.maple_attn_linear_workspace.argtypes, L.maple_attn_linear_workspace.restype = [I64] * 3, I64
+        L.maple_attn_linear_workspace.argtypes, L.maple_attn_linear_workspace.restype = [I64] * 3 + [I32], I64
         L.maple_attn_cached_workspace.argtypes, L.maple_attn_cached_workspace.restype = [I32] * 7, I64
         _fn = L
     return _fn
@@ -64,15 +67,16 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i:
 
 def _call(name: str, args: bytes, dev: int, stream) -> None:
     """Launch on `stream` or the device's current one, with that device current."""
-    fn = getattr(_fn or _lib(), "maple_attn_" + name)
+    if _fn is None:
+        _lib()
     if stream is None:
         stream = _raw_stream(dev)
     if dev == _current_device():
-        rc = fn(args, stream)
+        rc = _calls[name](args, stream)
     else:
         with torch.cuda.device(dev):
-            rc = fn(args, stream)
-    if rc != MAPLE_OK:
+            rc = _calls[name](args, stream)
+    if rc:
         raise MapleError(rc, "maple_attn_" + name)
 
 
@@ -105,6 +109,8 @@ def _vector(t, dtype, n: int, what: str) -> int:
     """Address of a contiguous vector of n values (0 for None)."""
     if t is None:
         return 0
+    if t.dtype is dtype and t.stride() == _UNIT and t.shape[0] == n:
+        return t.data_ptr()
     if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError(what)
     return t.data_ptr()
@@ -160,18 +166,18 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias
     if resid is not None and (resid.dtype is not torch.float32 or resid.shape != (T, N) or not resid.is_contiguous()):
         raise ValueError("resid must be contiguous fp32 [T][N]")
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype, device=x.device)
+        out = x.new_empty((T, N), dtype=out_dtype)
     elif out.shape != (T, N) or not out.is_contiguous():
         raise ValueError("out must be contiguous [T][N]")
     ydt = _OUT_TYPES.get(out.dtype)
     if ydt is None:
         raise ValueError("the output must be bf16 or fp32")
-    n = _size((_fn or _lib()).maple_attn_linear_workspace(T, K, N), "maple_attn_linear")
-    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    n = _size((_fn or _lib()).maple_attn_linear_workspace(T, K, N, 1 if normalise else 0), "maple_attn_linear")
+    ws = x.new_empty(n, dtype=torch.uint8) if n else None
     _call("linear", _LINEAR.pack(
         x.data_ptr(), weight.data_ptr(), _vector(alpha, torch.float32, N, "alpha must be fp32 [N]"),
         _vector(bias, torch.float32, N, "bias must be fp32 [N]"), 0 if resid is None else resid.data_ptr(), out.data_ptr(),
-        ws.data_ptr(), n, _flags(flags), x.stride(0) if T > 1 else K, T, K, N, ydt, 1 if normalise else 0), dev, stream)
+        0 if ws is None else ws.data_ptr(), n, _flags(flags), x.stride(0) if T > 1 else K, T, K, N, ydt, 1 if normalise else 0), dev, stream)
     return out
 
 
@@ -203,8 +209,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_
         n, P, vp, pp = _page_size(pages, Hkv, d), pages.shape[0], v.data_ptr(), pages.data_ptr()
     elif v is not None or slots is not None:
         raise ValueError("pages, v and slots go together")
-    qo = torch.empty((T, H, d), dtype=dt, device=q.device)
-    ko = torch.empty((T, Hkv, d), dtype=dt, device=q.device)
+    qo = q.new_empty((T, H, d))
+    ko = q.new_empty((T, Hkv, d))
     rot = inv_freq.shape[0]
     _call("qk_norm_rope", _ROPE.pack(
         q.data_ptr(), k.data_ptr(), vp, qo.data_ptr(), ko.data_ptr(),
@@ -228,8 +234,8 @@ def kv_read(pages: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: torc
     page_size = _page_size(pages, Hkv, head_dim)
     dev = _device(pages, slots, flags)
     n = slots.shape[0]
-    k = torch.empty((n, Hkv, head_dim), dtype=dtype, device=pages.device)
-    v = torch.empty((n, Hkv, head_dim), dtype=dtype, device=pages.device)
+    k = pages.new_empty((n, Hkv, head_dim), dtype=dtype)
+    v = torch.empty_like(k)
     _call("kv_read", _READ.pack(pages.data_ptr(), _vector(slots, torch.int64, n, "slots must be int64 [n]"), k.data_ptr(),
                                 v.data_ptr(), _flags(flags), n, P, Hkv, head_dim, page_size, _HEAD_TYPES[dtype]), dev, stream)
     return k, v
@@ -258,10 +264,10 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     if B < 0:
         raise ValueError("cu_q must be int32 [B+1]")
     if out is None:
-        out = torch.empty((Tq, H, d), dtype=dt, device=q.device)
+        out = q.new_empty((Tq, H, d))
     elif out.dtype is not dt or out.shape != (Tq, H, d) or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's type and shape")
-    lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device) if return_lse else None
+    lse = q.new_empty((Tq, H), dtype=torch.float32) if return_lse else None
     _call("prompt", _PROMPT.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
         _vector(cu_q, torch.int32, B + 1, "cu_q must be int32 [B+1]"), _vector(cu_k, torch.int32, B + 1, "cu_k must be int32 [B+1]"),
@@ -291,9 +297,9 @@ def cached_attention(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Te
             block_table.stride(1) != 1 and block_table.shape[1] > 1):
         raise ValueError("block_table must be int32 [B][max_pages]")
     mp = block_table.shape[1]
-    out = torch.empty((B, H, d), dtype=dt, device=q.device)
+    out = q.new_empty((B, H, d))
     w = _size((_fn or _lib()).maple_attn_cached_workspace(B, mp, H, Hkv, d, n, window), "maple_attn_cached")
-    ws = torch.empty(w, dtype=torch.uint8, device=q.device) if w else None
+    ws = q.new_empty(w, dtype=torch.uint8) if w else None
     _call("cached", _CACHED.pack(
         q.data_ptr(), out.data_ptr(), pages.data_ptr(), block_table.data_ptr(), _vector(lens, torch.int32, B, "lens must be int32 [B]"),
         0 if ws is None else ws.data_ptr(), w, _flags(flags), qs, block_table.stride(0) if B > 1 else mp, P, B, mp, H, Hkv, d, n, window,

@@ -26,8 +26,31 @@ namespace {
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
-// Int8 absmax codes of bf16 rows, one warp per row; the second pass over the
-// row hits L1 or L2.
+// Int8 absmax codes of bf16 rows, one warp per row.  NV > 0: the row (at most
+// 256 NV values) stays in registers between the maximum and the codes, all of
+// its loads in flight; NV = 0: longer rows are read twice, the second time from
+// L1 or L2.
+__device__ __forceinline__ uint2 quant8(const uint4 &v, float inv)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t pk[2] = {0u, 0u};
+#pragma unroll
+    for (int m = 0; m < 8; m++) {
+        const uint32_t bits = (m & 1) ? (w[m >> 1] >> 16) : (w[m >> 1] & 0xffffu);
+        pk[m >> 2] |= (uint32_t)(quant_code(bf16_bits_to_f32(bits), inv) & 0xff) << (8 * (m & 3));
+    }
+    return make_uint2(pk[0], pk[1]);
+}
+__device__ __forceinline__ float absmax8(const uint4 &v, float amax)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int m = 0; m < 4; m++)
+        amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(w[m] & 0xffffu)), fabsf(bf16_bits_to_f32(w[m] >> 16))));
+    return amax;
+}
+
+template <int NV>
 __global__ void __launch_bounds__(256) quantise_rows_kernel(const uint16_t *x, int64_t stride, int64_t T, int K, int8_t *q,
                                                             float *s)
 {
@@ -36,29 +59,26 @@ __global__ void __launch_bounds__(256) quantise_rows_kernel(const uint16_t *x, i
     asm volatile("griddepcontrol.launch_dependents;");
     if (t >= T) return;
     const uint4 *xr = reinterpret_cast<const uint4 *>(x + t * stride);
+    uint2 *qr = reinterpret_cast<uint2 *>(q + t * K);
+    const int n = K / 8;
+    uint4 v[NV > 0 ? NV : 1];
     float amax = 0.0f;
-    for (int c = lane; c < K / 8; c += 32) {
-        const uint4 v = __ldg(xr + c);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (NV > 0) {
 #pragma unroll
-        for (int m = 0; m < 4; m++) {
-            amax = fmaxf(amax, fabsf(bf16_bits_to_f32(w[m] & 0xffffu)));
-            amax = fmaxf(amax, fabsf(bf16_bits_to_f32(w[m] >> 16)));
-        }
+        for (int i = 0; i < NV; i++) v[i] = lane + 32 * i < n ? __ldg(xr + lane + 32 * i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < NV; i++) amax = absmax8(v[i], amax);
+    } else {
+        for (int c = lane; c < n; c += 32) amax = absmax8(__ldg(xr + c), amax);
     }
     amax = warp_max(amax);
-    const float inv = amax > 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;
-    for (int c = lane; c < K / 8; c += 32) {
-        const uint4 v = __ldg(xr + c);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t pk[2] = {0u, 0u};
+    const float inv = amax > 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;   // (a zero row: codes 0)
+    if (NV > 0) {
 #pragma unroll
-        for (int m = 0; m < 8; m++) {
-            const uint32_t bits = (m & 1) ? (w[m >> 1] >> 16) : (w[m >> 1] & 0xffffu);
-            const int code = amax > 0.0f ? quant_code(bf16_bits_to_f32(bits), inv) : 0;
-            pk[m >> 2] |= (uint32_t)(code & 0xff) << (8 * (m & 3));
-        }
-        reinterpret_cast<uint2 *>(q + t * K)[c] = make_uint2(pk[0], pk[1]);
+        for (int i = 0; i < NV; i++)
+            if (lane + 32 * i < n) qr[lane + 32 * i] = quant8(v[i], inv);
+    } else {
+        for (int c = lane; c < n; c += 32) qr[c] = quant8(__ldg(xr + c), inv);
     }
     if (lane == 0) s[t] = amax > 0.0f ? __fdiv_rn(amax, 127.0f) : 0.0f;
 }
@@ -574,23 +594,24 @@ int check_sizes(int64_t T, int64_t K, int64_t N)
 
 }  // namespace
 
-extern "C" int64_t maple_attn_linear_workspace(int64_t T, int64_t K, int64_t N)
+extern "C" int64_t maple_attn_linear_workspace(int64_t T, int64_t K, int64_t N, int32_t normalise)
 {
     const int rc = check_sizes(T, K, N);
     if (rc) return rc;
-    return round256(T * K) + round256(T * 4);   // (the largest need: few tokens are quantised in shared memory)
+    if (T == 0 || rows_path(T, (int)K, normalise != 0)) return 0;
+    return round256(T * K) + round256(T * 4);   // codes and scales
 }
 
 extern "C" int maple_attn_linear(const maple_attn_linear_args *args, maple_stream_t stream)
 {
     if (!args) return MAPLE_ERR_INVALID_ARG;
     const maple_attn_linear_args &a = *args;
-    const int64_t need = maple_attn_linear_workspace(a.T, a.K, a.N);
+    const int64_t need = maple_attn_linear_workspace(a.T, a.K, a.N, a.normalise);
     if (need < 0) return (int)need;
     if (a.normalise && a.K % 256) return MAPLE_ERR_UNSUPPORTED_SHAPE;
     if (a.y_dtype != MAPLE_BF16 && a.y_dtype != MAPLE_FP32) return MAPLE_ERR_INVALID_ARG;
     if (a.T == 0) return MAPLE_OK;
-    if (!a.x || !a.w || !a.alpha || !a.y || !a.workspace || a.workspace_bytes < need) return MAPLE_ERR_INVALID_ARG;
+    if (!a.x || !a.w || !a.alpha || !a.y || (need && (!a.workspace || a.workspace_bytes < need))) return MAPLE_ERR_INVALID_ARG;
     for (const void *p : {a.x, (const void *)a.w, (const void *)a.alpha, (const void *)a.bias, (const void *)a.resid,
                           (const void *)a.y, (const void *)a.workspace})
         if (!aligned16(p)) return MAPLE_ERR_INVALID_ARG;
@@ -635,7 +656,9 @@ extern "C" int maple_attn_linear(const maple_attn_linear_args *args, maple_strea
         norm_quantise_rows_kernel<<<(unsigned)((a.T + warps - 1) / warps), warps * 32, (size_t)warps * K * 2, st>>>(
             (const float *)a.x, a.x_stride, a.T, K, q, s);
     } else {
-        quantise_rows_kernel<<<(unsigned)((a.T + 7) / 8), 256, 0, st>>>((const uint16_t *)a.x, a.x_stride, a.T, K, q, s);
+        auto quantise = K <= 1024 ? quantise_rows_kernel<4> : K <= 2048 ? quantise_rows_kernel<8> : K <= 4096 ? quantise_rows_kernel<16>
+                                                                                               : quantise_rows_kernel<0>;
+        quantise<<<(unsigned)((a.T + 7) / 8), 256, 0, st>>>((const uint16_t *)a.x, a.x_stride, a.T, K, q, s);
     }
     cudaLaunchConfig_t lc;
     memset(&lc, 0, sizeof lc);

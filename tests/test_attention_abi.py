@@ -55,7 +55,7 @@ def call(lib, name, fields, **change):
         STRUCTS[name].pack(*fields.values()), None)
 
 
-LINEAR = dict(x=P, w=P, alpha=P, bias=0, resid=0, y=P, ws=P, wsb=1 << 20, flags=0, xs=64, T=2, K=64, N=8, dt=2, norm=0)
+LINEAR = dict(x=P, w=P, alpha=P, bias=0, resid=0, y=P, ws=P, wsb=1 << 20, flags=0, xs=64, T=20, K=64, N=8, dt=2, norm=0)
 ROPE = dict(q=P, k=P, v=P, qo=P, ko=P, qw=0, kw=0, pos=P, inv=P, pages=P, slots=P, flags=0, qs=512, ks=512, vs=512, T=2, NP=4,
             H=4, Hkv=2, d=128, rd=128, n=16, dt=0, inter=0, eps=1e-6)
 READ = dict(pages=P, slots=P, k=P, v=P, flags=0, n=2, NP=4, Hkv=2, d=128, ps=16, dt=0)
