@@ -59,9 +59,9 @@ template <int D>
 struct PromptSmem {
     static constexpr int kHalves = D / 64;                 // 64-column (128-byte) sub-tiles
     static constexpr int kTileBytes = kHalves * 128 * 128; // a Q, K or V tile
-    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kStages = D == 128 ? 2 : 4;       // pairs of a ring: K_j in the first half, V_j-1 in the second
     static constexpr int kKv = 2 * kTileBytes;             // after Q_A and Q_B
-    static constexpr int kBars = kKv + kStages * kTileBytes;
+    static constexpr int kBars = kKv + kStages * 2 * kTileBytes;
     static constexpr int kTotal = kBars + 512;
 };
 
@@ -289,16 +289,19 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     __shared__ Item s_items[kItems];
     __shared__ __align__(16) uint4 s_cancel;
     const maple_attn_prompt_args &a = p.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (a broadcast value is the same in a warp for the compiler too: the roles' code then counts as
+    // convergent and may use uniform registers)
+    const int warp = __shfl_sync(FULL, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if (smem_addr(smem) & 1023u) {   // the swizzled tiles need 1024-byte alignment
         if (threadIdx.x == 0) set_flag(a.flags, MAPLE_DEVFLAG_TIMEOUT);
         return;
     }
     uint64_t *bars = (uint64_t *)(smem + L::kBars);
     const uint32_t b_full = smem_addr(bars), b_empty = b_full + 8 * S, b_q = b_empty + 8 * S, b_qfree = b_q + 8;
-    const uint32_t b_s = b_qfree + 8, b_p = b_s + 16, b_o = b_p + 32, b_item = b_o + 16, b_ifree = b_item + 8 * kItems;
-    const uint32_t b_cancel = b_ifree + 8 * kItems, b_drain = b_cancel + 8, b_next = b_drain + 8;
-    uint32_t *tmem_holder = (uint32_t *)(bars + 2 * S + 2 + 2 + 4 + 2 + 2 * kItems + 3);
+    const uint32_t b_s = b_qfree + 8, b_p = b_s + 16, b_pv = b_p + 16, b_item = b_pv + 16, b_ifree = b_item + 8 * kItems;
+    const uint32_t b_cancel = b_ifree + 8 * kItems, b_drain = b_cancel + 8, b_next = b_drain + 8,
+                   b_sfree = b_next + 8;
+    uint32_t *tmem_holder = (uint32_t *)(bars + 2 * S + 2 + 2 + 2 + 2 + 2 * kItems + 4);
     volatile uint32_t *abort = tmem_holder + 1;
     uint32_t *odd_values = tmem_holder + 2;   // [2 items] something in V was not finite
     const uint64_t limit = kDefaultWaitNs;
@@ -312,9 +315,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         mbar_init(b_qfree, 1);
         for (int i = 0; i < 2; i++) {
             mbar_init(b_s + 8 * i, 1);
-            mbar_init(b_p + 16 * i, 4);       // first half of P
-            mbar_init(b_p + 16 * i + 8, 4);   // second half
-            mbar_init(b_o + 8 * i, 1);
+            mbar_init(b_p + 8 * i, 4);
+            mbar_init(b_pv + 8 * i, 1);
         }
         for (int i = 0; i < kItems; i++) {
             mbar_init(b_item + 8 * i, 1);
@@ -324,6 +326,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         mbar_init(b_cancel, 1);
         mbar_init(b_drain, 1);
         mbar_init(b_next, 1);
+        mbar_init(b_sfree, 4);
         *abort = 0u;
         fence_barrier_init();
     }
@@ -332,7 +335,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    constexpr uint32_t kO = 256;   // first column of O_A
+    constexpr uint32_t kP = 128, kO = 256;   // first columns of P_A and O_A (S: column 0)
 
     // the u-th item of this CTA, as the scheduling warp wrote it (false: a wait gave up)
     auto get_item = [&](int u, Item &it) -> bool {
@@ -392,12 +395,11 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         // and products' operands have to be (moving them there cost a fifth of the kernel's time).
         if (lane == 0) {
             Item w;
-            int u = -1, j = 0, n = 0, nq = 0, kbeg = 0;
+            int u = -1, j = 0, n = -1, nq = 0, kbeg = 0;
             bool ok = true;
-            uint32_t it = 0;
-            for (;; it++, j++) {   // tiles K_j and V_j, ring positions 2 it and 2 it + 1
+            for (uint32_t it = 0;; it++, j++) {   // pair it of the ring: K_j (j < n) and V_j-1 (j > 0), n + 1 pairs for an item
                 bool done = false;
-                while (j == n) {
+                while (j == n + 1) {
                     if (u >= 0) {
                         drop_item(u);
                         mbar_arrive(b_next);
@@ -408,8 +410,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                         break;
                     }
                     const Range g(w, p.nt, a.window);
-                    j = 0;
                     n = w.kvh >= 0 ? g.n : 0;
+                    j = n > 0 ? 0 : n + 1;
                     kbeg = g.kbeg;
                     if (n > 0) {
                         if (!(ok = mbar_wait(b_qfree, (nq & 1) ^ 1, abort, a.flags, limit))) {
@@ -425,16 +427,16 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     }
                 }
                 if (done) break;
-#pragma unroll
-                for (int kv = 0; kv < 2; kv++) {
-                    const uint32_t t = 2 * it + kv, s = t % S;
-                    if (!(ok = ok && mbar_wait(b_empty + 8 * s, ((t / S) & 1) ^ 1, abort, a.flags, limit))) break;
-                    mbar_expect_tx(b_full + 8 * s, L::kTileBytes);
+                const uint32_t s = it % S;
+                if (!(ok = mbar_wait(b_empty + 8 * s, ((it / S) & 1) ^ 1, abort, a.flags, limit))) break;
+                mbar_expect_tx(b_full + 8 * s, (j > 0 && j < n ? 2 : 1) * L::kTileBytes);
+                const uint32_t dst = smem_addr(smem + L::kKv + s * 2 * L::kTileBytes);
+                const int row = w.k0 + kbeg + j * kKeys;
+                if (j < n)
+                    for (int h = 0; h < L::kHalves; h++) tma_load_3d(dst + h * 16384, &k_map, 64 * h, w.kvh, row, b_full + 8 * s);
+                if (j > 0)
                     for (int h = 0; h < L::kHalves; h++)
-                        tma_load_3d(smem_addr(smem + L::kKv + s * L::kTileBytes + h * 16384), kv ? &v_map : &k_map, 64 * h, w.kvh,
-                                    w.k0 + kbeg + j * kKeys, b_full + 8 * s);
-                }
-                if (!ok) break;
+                        tma_load_3d(dst + L::kTileBytes + h * 16384, &v_map, 64 * h, w.kvh, row - kKeys, b_full + 8 * s);
             }
             if (*abort) {   // drain the copies in flight: whatever was asked of a barrier arrives or runs out of time
                 for (int q = 0; q < S + 1; q++) {
@@ -454,88 +456,101 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         const bool leader = elect_one();
         const bool bf = __is_same(T, __nv_bfloat16);
         const uint32_t id_s = idesc_f16(bf, kKeys, false), id_o = idesc_f16(bf, D, true);
-        const uint32_t tm = __shfl_sync(FULL, tmem, 0);
-        const uint64_t dq = desc_sw128(smem_addr(smem)), dk = desc_sw128(smem_addr(smem + L::kKv)), dv = desc_mn_sw128(smem_addr(smem + L::kKv));
+        const uint32_t tm = __reduce_max_sync(FULL, tmem);   // (a warp reduction's result is in a uniform register)
+        const uint64_t dq = desc_sw128(smem_addr(smem)), dk = desc_sw128(smem_addr(smem + L::kKv));
+        const uint64_t dv = desc_mn_sw128(smem_addr(smem + L::kKv + L::kTileBytes));
         constexpr uint64_t kStep = L::kTileBytes / 16;   // a tile in descriptor units
-        int u = -1, j = 0, n = 0, ni = 0;
-        uint32_t it = 0, phB = 0, nq = 0;      // tiles so far (the phase of P_A), tiles with a B, items with a Q
-        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(FULL, mbar_wait(bar, parity, abort, a.flags, limit)); };
+        int u = -1, j = 0, n = -1, ni = 0;
+        // pairs so far, tiles of A and of B (the phases of P), items with a Q, products into S
+        uint32_t it = 0, phA = 0, phB = 0, nq = 0, nscore = 0;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            if (__all_sync(FULL, mbar_poll(bar, parity))) return true;
+            return (bool)__all_sync(FULL, mbar_wait(bar, parity, abort, a.flags, limit));
+        };
         auto commit = [&](uint32_t bar) {
             if (leader) mma_commit(bar);
             __syncwarp();
         };
-        // S_i = Q_i K^T of stage s; O_i += P_i V, 64 keys of the V of stage s
-        auto scores = [&](int i, uint32_t s) {
-            const uint64_t da = dq + i * kStep, db = dk + s * kStep;
+        // S = Q_i K^T of stage s, once the rows of the scores before have been taken out of S
+        auto scores = [&](int i, uint32_t s) -> bool {
+            if (nscore > 0 && !wait(b_sfree, (nscore - 1) & 1)) return false;
+            nscore++;
+            tc_fence_after();
+            const uint64_t da = dq + i * kStep, db = dk + s * (2 * kStep);
             if (leader) {
 #pragma unroll
                 for (int k = 0; k < D / 16; k++)
-                    mma_ss(tm + 128 * i, da + (k / 4) * 1024 + 2 * (k % 4), db + (k / 4) * 1024 + 2 * (k % 4), id_s, k != 0);
+                    mma_ss(tm, da + (k / 4) * 1024 + 2 * (k % 4), db + (k / 4) * 1024 + 2 * (k % 4), id_s, k != 0);
                 mma_commit(b_s + 8 * i);
             }
             __syncwarp();
+            return true;
         };
-        auto values = [&](int i, uint32_t s, int half, bool first) {
-            const uint64_t db = dv + s * kStep;
+        // O_i += P_i V of stage s
+        auto values = [&](int i, uint32_t s, bool first) {
+            const uint64_t db = dv + s * (2 * kStep);
             if (leader) {
 #pragma unroll
-                for (int k = 4 * half; k < 4 * half + 4; k++)
-                    mma_ts(tm + kO + D * i, tm + 128 * i + 8 * k, db + 128 * k, id_o, k > 0 || !first);
+                for (int k = 0; k < kKeys / 16; k++)
+                    mma_ts(tm + kO + D * i, tm + kP + 64 * i + 8 * k, db + 128 * k, id_o, k > 0 || !first);
+                mma_commit(b_pv + 8 * i);
             }
             __syncwarp();
         };
+        // Pair `it` of the ring holds K_j and V_j-1.  A step issues S = Q K_j and then O += P V_j-1
+        // for A and for B, so that scores are computed while the rows of the tile before are in the
+        // exponentials.  The stage is released and the next pair waited for behind the products of B,
+        // while the tensor cores are still busy.
+        bool ready = false;          // pair `it` has arrived
         for (;; it++, j++) {
             bool done = false;
-            while (j == n) {
+            while (j == n + 1) {
                 if (u >= 0 && leader) drop_item(u);
                 u++;
                 Item w;
                 const bool got = get_item(u, w);
-                if (!__all_sync(FULL, got) || __shfl_sync(FULL, w.kvh, 0) == -1) {
+                if (!__all_sync(FULL, got && w.kvh != -1)) {
                     done = true;
                     break;
                 }
                 const Range g(w, p.nt, a.window);
-                j = 0;
-                n = __shfl_sync(FULL, w.kvh >= 0 ? g.n : 0, 0);
-                ni = __shfl_sync(FULL, g.hasB ? 2 : 1, 0);
+                n = __reduce_max_sync(FULL, w.kvh >= 0 ? g.n : 0);
+                ni = __reduce_max_sync(FULL, g.hasB ? 2 : 1);
+                j = n > 0 ? 0 : n + 1;
+                if (n > 0) {
+                    if (!wait(b_q, nq & 1)) {
+                        done = true;
+                        break;
+                    }
+                    nq++;
+                }
             }
             if (done) break;
-            const uint32_t tk = 2 * it, tv = tk + 1, tn = tk + 2;     // ring positions of K_j, V_j and K_j+1
-            if (j == 0) {
-                if (!wait(b_q, nq & 1) || !wait(b_full + 8 * (tk % S), (tk / S) & 1)) break;
-                nq++;
-                tc_fence_after();
-                scores(0, tk % S);
-                if (ni == 2) scores(1, tk % S);
-                commit(b_empty + 8 * (tk % S));
-                if (n == 1) commit(b_qfree);
-            }
-            const bool more = j + 1 < n;
-            if (!wait(b_full + 8 * (tv % S), (tv / S) & 1) || (more && !wait(b_full + 8 * (tn % S), (tn / S) & 1))) break;
+            const uint32_t s = it % S;
+            if (!ready && !wait(b_full + 8 * s, (it / S) & 1)) break;
             bool ok = true;
 #pragma unroll
             for (int i = 0; i < 2; i++) {
                 if (i == 0 || ni == 2) {
-#pragma unroll
-                    for (int half = 0; half < 2; half++) {
-                        ok = ok && wait(b_p + 16 * i + 8 * half, (i == 0 ? it : phB) & 1);
+                    if (j < n) ok = ok && scores(i, s);
+                    if (j > 0) {
+                        ok = ok && wait(b_p + 8 * i, (i == 0 ? phA : phB) & 1);
                         if (ok) {
                             tc_fence_after();
-                            values(i, tv % S, half, j == 0);
+                            values(i, s, j == 1);
                         }
-                    }
-                    if (ok) {
-                        if (more) scores(i, tn % S);
-                        else commit(b_o + 8 * i);
                     }
                 }
             }
-            if (ni == 2) phB++;
             if (!ok) break;
-            commit(b_empty + 8 * (tv % S));
-            if (more) commit(b_empty + 8 * (tn % S));
-            if (j + 2 == n) commit(b_qfree);   // the last scores are issued
+            if (j > 0) {
+                phA++;
+                if (ni == 2) phB++;
+            }
+            commit(b_empty + 8 * s);
+            if (j + 1 == n) commit(b_qfree);   // the last scores are issued
+            ready = j < n && wait(b_full + 8 * ((it + 1) % S), ((it + 1) / S) & 1);
+            if (j < n && !ready) break;
         }
         commit(b_drain);   // every issued MMA has finished before tensor memory is released
         const uint64_t c0 = global_ns();
@@ -548,11 +563,11 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       const int i = warp >> 2, r = threadIdx.x & 127;
       const int rt = r / p.G, h = r - rt * p.G;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t ts = tmem + 128 * i + lanes, to = tmem + kO + D * i + lanes;
+      const uint32_t ts = tmem + lanes, tp = tmem + kP + 64 * i + lanes, to = tmem + kO + D * i + lanes;
       const bool neg = a.scale < 0.0f;
       const float scale2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);   // (0 as 10^-30: -inf stays -inf)
-      int t0 = 0;                 // ring position of the item's K_0
-      uint32_t ns = 0, no = 0;    // phases of S_i and O_i
+      uint32_t t0 = 0;            // ring position of the item's first pair
+      uint32_t ns = 0;            // tiles of this half so far: the phase of S_i, P_i and O_i
       bool ok = true;
       for (int u = 0; ok; u++) {
         Item w;
@@ -568,10 +583,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 const bool edge = g.masked(w, a.window, j);
                 if (edge && i == 0) {
                     // V_j: what is not finite becomes 0 before the products read it
-                    const int t = t0 + 2 * j + 1;
+                    const uint32_t t = t0 + j + 1;       // (V_j comes with K_j+1)
                     if (!mbar_wait(b_full + 8 * (t % S), (t / S) & 1, abort, a.flags, limit)) ok = false;
                     if (ok) {
-                        uint4 *tile = (uint4 *)(smem + L::kKv + (t % S) * L::kTileBytes);
+                        uint4 *tile = (uint4 *)(smem + L::kKv + ((t % S) * 2 + 1) * L::kTileBytes);
                         bool any = false;
 #pragma unroll 4
                         for (int c = threadIdx.x; c < L::kTileBytes / 16; c += 128) {
@@ -596,6 +611,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
 #pragma unroll
                 for (int c = 0; c < kKeys; c += 32) tmem_ld32(ts + c, *reinterpret_cast<int(*)[32]>(&s[c]));
                 tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_sfree);   // the next scores may be written
                 if (neg) {
 #pragma unroll
                     for (int c = 0; c < kKeys; c++) s[c] = -s[c];
@@ -612,6 +630,11 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
 #pragma unroll
                 for (int c = 12; c < kKeys; c += 2) mx[(c / 2) & 3] = max3(mx[(c / 2) & 3], s[c], s[c + 1]);
                 const float mt = max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * scale2;
+                // the products of the tile before have read P and updated O
+                if (j > 0) ok = mbar_wait(b_pv + 8 * i, ns & 1, abort, a.flags, limit);
+                ok = __all_sync(FULL, ok);
+                if (!ok) break;
+                tc_fence_after();
                 const bool up = mt > m + 8.0f;
                 if (__any_sync(FULL, up)) {
                     const float f = !up ? 1.0f : (m == -INFINITY ? 0.0f : ex2(m - mt));
@@ -645,20 +668,18 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                         sum[(e / 2) & 1] = add2(sum[(e / 2) & 1], pair(p0, p1));
                         pk[e / 2] = Elem<T>::pack(p0, p1);
                     }
-                    // (S and P share columns: every S of the row is in registers by now)
-                    tmem_st32(ts + c / 2, pk);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(b_p + 16 * i + c / 8);
+                    tmem_st32(tp + c / 2, pk);
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_p + 8 * i);
                 float s0, s1;
                 unpair(add2(sum[0], sum[1]), s0, s1);
                 l += s0 + s1;
             }
             if (n > 0) {
-                ok = ok && mbar_wait(b_o + 8 * i, no & 1, abort, a.flags, limit);
-                no++;
+                ok = ok && mbar_wait(b_pv + 8 * i, (ns - 1) & 1, abort, a.flags, limit);
             }
             ok = __all_sync(FULL, ok);
             if (!ok) break;
@@ -706,7 +727,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             if (valid && a.lse) a.lse[row] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             tc_fence_before();   // O is read before the next item's first product writes it (ordered by P's barrier)
         }
-        t0 += 2 * n;
+        if (n > 0) t0 += n + 1;
         __syncwarp();
         if (lane == 0) drop_item(u);
       }

@@ -35,6 +35,19 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
         : "memory");
     return ok != 0;
 }
+// the same without suspending the thread: a poll of a phase that is expected to be complete
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ uint64_t global_ns() { return global_timer_ns(); }
 
 // Wait for the phase of `bar` with the given parity to complete.  Gives up
