@@ -273,9 +273,8 @@ linear_rows_kernel(const uint16_t *x, int64_t x_stride, int T, int K, const int8
 // 128 bytes of K by TMA with the 128-byte swizzle, int32 accumulators in tensor
 // memory, two of them, so that the epilogue of a tile runs under the next one's
 // products.  SWAP: A is the weights and B the tokens (T <= 128), else the other
-// way round.  Warp 0 loads, warp 1 issues the products (the whole warp with the
-// same values in every lane and one lane issuing: the operands have to be in
-// uniform registers), warps 4-11 scale and store.  CTAs take tiles round robin.
+// way round.  Warp 0 loads, warp 1 issues the products, warps 4-11 scale and
+// store.  CTAs take tiles round robin.
 // ---------------------------------------------------------------------------
 constexpr int kGemmThreads = 384, kGemmBK = 128;
 
@@ -309,7 +308,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 linear_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map, const GemmArgs p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (a broadcast index: the products' operands stay in uniform registers)
+    const int warp = __shfl_sync(FULL, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if (smem_addr(smem) & 1023u) {   // the swizzled tiles need 1024-byte alignment
         if (threadIdx.x == 0) set_flag(p.flag, MAPLE_DEVFLAG_TIMEOUT);
         return;
@@ -390,37 +390,36 @@ linear_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_const
         }
     } else if (warp == 1) {
         // ---------------- products
-        const bool leader = elect_one();
-        const uint32_t tm = __shfl_sync(FULL, tmem, 0), idesc = idesc_i8(bn);
-        const uint64_t d0 = desc_sw128(smem_addr(smem));
-        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(FULL, mbar_wait(bar, parity, abort, p.flag, limit)); };
-        uint32_t wrap = 0, n = 0;
-        int s = 0;
-        bool ok = true;
-        for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, n++) {
-            const uint32_t d = tm + 256 * (n & 1);
-            if (!(ok = wait(b_free + 8 * (n & 1), ((n >> 1) & 1) ^ 1))) break;
-            for (int k = 0; k < KS; k++) {
-                if (!(ok = wait(b_full + 8 * s, wrap & 1))) break;
-                tc_fence_after();
-                const uint64_t da = d0 + (uint64_t)(s * (stage_bytes / 16)), db = da + 128 * kGemmBK / 16;
-                if (leader) {
+        if (elect_one()) {
+            const uint32_t idesc = idesc_i8(bn);
+            const uint64_t d0 = desc_sw128(smem_addr(smem));
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                return mbar_poll(bar, parity) || mbar_wait(bar, parity, abort, p.flag, limit);
+            };
+            uint32_t wrap = 0, n = 0;
+            int s = 0;
+            bool ok = true;
+            for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, n++) {
+                const uint32_t d = tmem + 256 * (n & 1);
+                if (!(ok = wait(b_free + 8 * (n & 1), ((n >> 1) & 1) ^ 1))) break;
+                for (int k = 0; k < KS; k++) {
+                    if (!(ok = wait(b_full + 8 * s, wrap & 1))) break;
+                    tc_fence_after();
+                    const uint64_t da = d0 + (uint64_t)(s * (stage_bytes / 16)), db = da + 128 * kGemmBK / 16;
 #pragma unroll
                     for (int q = 0; q < kGemmBK / 32; q++) mma_i8_plain(d, da + 2 * q, db + 2 * q, idesc, k > 0 || q > 0);
                     mma_commit(b_empty + 8 * s);
                     if (k + 1 == KS) mma_commit(b_acc + 8 * (n & 1));
-                }
-                __syncwarp();
-                if (++s == S) {
-                    s = 0;
-                    wrap++;
+                    if (++s == S) {
+                        s = 0;
+                        wrap++;
+                    }
                 }
             }
-        }
-        if (leader) mma_commit(b_drain);   // every issued MMA has finished before tensor memory is released
-        __syncwarp();
-        const uint64_t c0 = global_ns();
-        while (!mbar_test(b_drain, 0) && global_ns() - c0 < limit) {
+            mma_commit(b_drain);   // every issued MMA has finished before tensor memory is released
+            const uint64_t c0 = global_ns();
+            while (!mbar_test(b_drain, 0) && global_ns() - c0 < limit) {
+            }
         }
     } else if (warp >= 4) {
         // ---------------- epilogue: lane quarter warp % 4, every other 32 columns

@@ -15,18 +15,16 @@
 //
 // One CTA works on two tiles (A and B, consecutive tokens) of a sequence and a
 // key/value head, over tiles of 128 keys:
-//   warp 8    TMA: Q once, then K_0, V_0, K_1, V_1, ... into a ring
-//   warp 9    MMA: S_A = Q_A K_0, S_B = Q_B K_0, then per key tile j
-//             O_A += P_A V_j, S_A = Q_A K_j+1, O_B += P_B V_j, S_B = Q_B K_j+1
 //   warps 0-3 softmax of A, warps 4-7 of B: one thread per row, S from tensor
-//             memory, P back over the same columns, handed over in two halves;
-//             rescaling and the epilogue
+//             memory, P back; rescaling and the epilogue
+//   warp 8    TMA: Q once, then pairs (K_j, V_j-1) into a ring
+//   warp 9    MMA, per pair: S = Q_A K_j, O_A += P_A V_j-1, the same for B
 //   warp 10   the CTA's items, one ahead: the loads and first products of the
 //             next item run under the last softmax and epilogue of this one
 // While one tile's rows are in the exponentials, the tensor cores work on the
-// other's products.  Tensor memory: S_A, S_B (P over their first half), O_A,
-// O_B = 512 columns at d = 128.  In-order execution of the MMAs makes "S_j full"
-// imply that O has taken V_j-1.
+// other's products and on this one's next scores: tensor memory holds one S that
+// A and B use in turn (it is free again as soon as its rows are in registers),
+// P_A, P_B, O_A and O_B: 512 columns at d = 128.
 //
 // Masked keys.  P is 0 there, but 0 times an infinity or NaN in V would reach
 // the sums; so tiles that hold masked keys have what is not finite in V set to
@@ -449,10 +447,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         }
       } else if (warp == 9) {
         // ---------------- products
-        // The whole warp runs this with values that are the same in every lane (votes, broadcasts,
-        // loop counters), and one lane issues: the operands of the products then stay in uniform
-        // registers.  With one lane running it all they were moved there one by one, and issuing
-        // them was what the kernel waited for.
+        // One elected lane of a warp whose index is a broadcast: the compiler then keeps the products'
+        // operands in uniform registers.  (Without the broadcast they were moved there one by one,
+        // 80 clocks a product; with all lanes running it, votes and reconvergence cost 100 clocks a wait.)
         const bool leader = elect_one();
         const bool bf = __is_same(T, __nv_bfloat16);
         const uint32_t id_s = idesc_f16(bf, kKeys, false), id_o = idesc_f16(bf, D, true);
@@ -460,16 +457,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         const uint64_t dq = desc_sw128(smem_addr(smem)), dk = desc_sw128(smem_addr(smem + L::kKv));
         const uint64_t dv = desc_mn_sw128(smem_addr(smem + L::kKv + L::kTileBytes));
         constexpr uint64_t kStep = L::kTileBytes / 16;   // a tile in descriptor units
+        if (leader) {
         int u = -1, j = 0, n = -1, ni = 0;
         // pairs so far, tiles of A and of B (the phases of P), items with a Q, products into S
         uint32_t it = 0, phA = 0, phB = 0, nq = 0, nscore = 0;
         auto wait = [&](uint32_t bar, uint32_t parity) {
-            if (__all_sync(FULL, mbar_poll(bar, parity))) return true;
-            return (bool)__all_sync(FULL, mbar_wait(bar, parity, abort, a.flags, limit));
+            return mbar_poll(bar, parity) || mbar_wait(bar, parity, abort, a.flags, limit);
         };
         auto commit = [&](uint32_t bar) {
-            if (leader) mma_commit(bar);
-            __syncwarp();
+            mma_commit(bar);
         };
         // S = Q_i K^T of stage s, once the rows of the scores before have been taken out of S
         auto scores = [&](int i, uint32_t s) -> bool {
@@ -477,25 +473,23 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             nscore++;
             tc_fence_after();
             const uint64_t da = dq + i * kStep, db = dk + s * (2 * kStep);
-            if (leader) {
+            {
 #pragma unroll
                 for (int k = 0; k < D / 16; k++)
                     mma_ss(tm, da + (k / 4) * 1024 + 2 * (k % 4), db + (k / 4) * 1024 + 2 * (k % 4), id_s, k != 0);
                 mma_commit(b_s + 8 * i);
             }
-            __syncwarp();
             return true;
         };
         // O_i += P_i V of stage s
         auto values = [&](int i, uint32_t s, bool first) {
             const uint64_t db = dv + s * (2 * kStep);
-            if (leader) {
+            {
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; k++)
                     mma_ts(tm + kO + D * i, tm + kP + 64 * i + 8 * k, db + 128 * k, id_o, k > 0 || !first);
                 mma_commit(b_pv + 8 * i);
             }
-            __syncwarp();
         };
         // Pair `it` of the ring holds K_j and V_j-1.  A step issues S = Q K_j and then O += P V_j-1
         // for A and for B, so that scores are computed while the rows of the tile before are in the
@@ -505,17 +499,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         for (;; it++, j++) {
             bool done = false;
             while (j == n + 1) {
-                if (u >= 0 && leader) drop_item(u);
+                if (u >= 0) drop_item(u);
                 u++;
                 Item w;
                 const bool got = get_item(u, w);
-                if (!__all_sync(FULL, got && w.kvh != -1)) {
+                if (!got || w.kvh == -1) {
                     done = true;
                     break;
                 }
                 const Range g(w, p.nt, a.window);
-                n = __reduce_max_sync(FULL, w.kvh >= 0 ? g.n : 0);
-                ni = __reduce_max_sync(FULL, g.hasB ? 2 : 1);
+                n = w.kvh >= 0 ? g.n : 0;
+                ni = g.hasB ? 2 : 1;
                 j = n > 0 ? 0 : n + 1;
                 if (n > 0) {
                     if (!wait(b_q, nq & 1)) {
@@ -555,6 +549,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         commit(b_drain);   // every issued MMA has finished before tensor memory is released
         const uint64_t c0 = global_ns();
         while (!mbar_test(b_drain, 0) && global_ns() - c0 < limit) {
+        }
         }
       }
     } else {
