@@ -284,6 +284,7 @@ struct GemmArgs {
     int64_t T;
     int K, bn, stages;
     int64_t tiles_a, tiles_b;
+    int y_tma;                 // y is written by TMA (its rows are multiples of 16 bytes)
     unsigned *flag;
 };
 
@@ -303,9 +304,17 @@ __device__ __forceinline__ void mma_i8_plain(uint32_t d_tmem, uint64_t adesc, ui
         : "memory");
 }
 
+// four values from index i on, 0 beyond n
+__device__ __forceinline__ float4 load4(const float *p, int64_t i, int64_t n)
+{
+    if (i + 4 <= n) return *reinterpret_cast<const float4 *>(p + i);
+    return make_float4(i < n ? p[i] : 0.0f, i + 1 < n ? p[i + 1] : 0.0f, i + 2 < n ? p[i + 2] : 0.0f, 0.0f);
+}
+
 template <bool SWAP>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-linear_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map, const GemmArgs p)
+linear_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
+                   const __grid_constant__ CUtensorMap y_map, const GemmArgs p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     // (a broadcast index: the products' operands stay in uniform registers)
@@ -316,7 +325,9 @@ linear_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_const
     }
     const int S = p.stages, bn = p.bn;
     const uint32_t stage_bytes = (128 + bn) * kGemmBK;
-    uint64_t *bars = (uint64_t *)(smem + S * stage_bytes);
+    uint8_t *s_out = smem + S * stage_bytes;                       // [8 epilogue warps][4 KB] rows on their way to y
+    float *s_cols = (float *)(s_out + (SWAP ? 0 : 8 * 4096));      // [8 warps][alpha, bias][128]: the warp's columns of a tile
+    uint64_t *bars = (uint64_t *)((uint8_t *)s_cols + (SWAP ? 0 : 8 * 1024));
     const uint32_t b_full = smem_addr(bars), b_empty = b_full + 8 * S, b_acc = b_empty + 8 * S, b_free = b_acc + 16, b_drain = b_free + 16;
     uint32_t *tmem_holder = (uint32_t *)(bars + 2 * S + 5);
     volatile uint32_t *abort = tmem_holder + 1;
@@ -432,6 +443,18 @@ linear_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_const
             const int64_t row = ta * 128 + r;
             const bool in = row < (SWAP ? o.N : p.T);
             const float fr = in ? (SWAP ? __ldg(o.alpha + row) : __ldg(p.s + row)) : 0.0f;
+            float *my_alpha = s_cols + (warp - 4) * 256, *my_bias = my_alpha + 128;
+            if (!SWAP) {   // the columns' scales, loaded while the products run
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int64_t c = tb * bn + 32 * half + 64 * i + lane;
+                    const bool on = 32 * half + 64 * i < bn && c < o.N;
+                    my_alpha[32 * i + lane] = on ? __ldg(o.alpha + c) : 0.0f;
+                    my_bias[32 * i + lane] = on && o.bias ? __ldg(o.bias + c) : 0.0f;
+                }
+                __syncwarp();
+            }
             if (!__all_sync(FULL, mbar_wait(b_acc + 8 * (n & 1), (n >> 1) & 1, abort, p.flag, limit))) break;
             tc_fence_after();
             const uint32_t src = tmem + 256 * (n & 1) + ((uint32_t)(32 * q) << 16);
@@ -445,13 +468,18 @@ linear_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_const
 #pragma unroll
                     for (int c = 0; c < 32; c++)
                         if (in && col + c < p.T) o.store(col + c, row, acc[c], __ldg(p.s + col + c));
-                } else if (in) {
+                } else {
                     // lane = token, columns = channels
                     float v[32];
-                    if (col + 32 <= o.N && (o.N & 7) == 0) {
+                    if (p.y_tma) {
+                        // 32 rows x 32 channels through shared memory, so that y is written in whole
+                        // row pieces: stored by the lanes (16 bytes of 32 rows at a time), the
+                        // epilogue took longer than the products
+                        const float4 *al4 = reinterpret_cast<const float4 *>(my_alpha + (c0 >> 6) * 32);
+                        const float4 *bi4 = reinterpret_cast<const float4 *>(my_bias + (c0 >> 6) * 32);
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
-                            const float4 al = __ldg(reinterpret_cast<const float4 *>(o.alpha + col + c));
+                            const float4 al = al4[c / 4];
                             v[c] = __fmul_rn((float)acc[c], __fmul_rn(al.x, fr));
                             v[c + 1] = __fmul_rn((float)acc[c + 1], __fmul_rn(al.y, fr));
                             v[c + 2] = __fmul_rn((float)acc[c + 2], __fmul_rn(al.z, fr));
@@ -460,25 +488,31 @@ linear_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_const
                         if (o.bias) {
 #pragma unroll
                             for (int c = 0; c < 32; c += 4) {
-                                const float4 bi = __ldg(reinterpret_cast<const float4 *>(o.bias + col + c));
+                                const float4 bi = bi4[c / 4];
                                 v[c] = __fadd_rn(v[c], bi.x);
                                 v[c + 1] = __fadd_rn(v[c + 1], bi.y);
                                 v[c + 2] = __fadd_rn(v[c + 2], bi.z);
                                 v[c + 3] = __fadd_rn(v[c + 3], bi.w);
                             }
                         }
-                        if (o.resid) {
+                        if (o.resid && in) {
 #pragma unroll
                             for (int c = 0; c < 32; c += 4) {
-                                const float4 re = *reinterpret_cast<const float4 *>(o.resid + row * o.N + col + c);
+                                const float4 re = load4(o.resid + row * o.N, col + c, o.N);
                                 v[c] = __fadd_rn(re.x, v[c]);
                                 v[c + 1] = __fadd_rn(re.y, v[c + 1]);
                                 v[c + 2] = __fadd_rn(re.z, v[c + 2]);
                                 v[c + 3] = __fadd_rn(re.w, v[c + 3]);
                             }
                         }
-                        if (o.y_bf16) {
-                            uint4 *dst = reinterpret_cast<uint4 *>((uint16_t *)o.y + row * o.N + col);
+                        // (two pieces of bf16 fit the warp's 4 KB, one of fp32: the piece before has left it)
+                        uint8_t *st = s_out + (warp - 4) * 4096 + (o.y_bf16 ? ((c0 >> 6) & 1) * 2048 : 0);
+                        if (lane == 0) {
+                            if (o.y_bf16) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                            else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        }
+                        __syncwarp();
+                        if (o.y_bf16) {      // rows of 64 bytes, 64-byte swizzle
 #pragma unroll
                             for (int c = 0; c < 32; c += 8) {
                                 uint32_t w[4];
@@ -487,14 +521,23 @@ linear_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_const
                                     const __nv_bfloat162 b = __floats2bfloat162_rn(v[c + 2 * z], v[c + 2 * z + 1]);
                                     w[z] = *reinterpret_cast<const uint32_t *>(&b);
                                 }
-                                dst[c / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                                *reinterpret_cast<uint4 *>(st + lane * 64 + (((c / 8) ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                             }
-                        } else {
-                            float4 *dst = reinterpret_cast<float4 *>((float *)o.y + row * o.N + col);
+                        } else {             // rows of 128 bytes, 128-byte swizzle
 #pragma unroll
-                            for (int c = 0; c < 32; c += 4) dst[c / 4] = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                            for (int c = 0; c < 32; c += 4)
+                                *reinterpret_cast<float4 *>(st + lane * 128 + (((c / 4) ^ (lane & 7)) << 4)) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
                         }
-                    } else {
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && ta * 128 + 32 * q < p.T && col < o.N) {   // (rows and columns beyond y are cut off)
+                            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                                             reinterpret_cast<uint64_t>(&y_map)),
+                                         "r"(smem_addr(st)), "r"((int)col), "r"((int)(ta * 128 + 32 * q))
+                                         : "memory");
+                        }
+                        if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");   // (an empty one too: they are counted)
+                    } else if (in) {
 #pragma unroll
                         for (int c = 0; c < 32; c++)
                             if (col + c < o.N) o.store(row, col + c, acc[c], fr);
@@ -505,6 +548,8 @@ linear_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(b_free + 8 * (n & 1));
         }
+        // (shared memory must outlive the stores that read it)
+        if (!SWAP && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
@@ -518,8 +563,7 @@ typedef CUresult (*encode_fn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, vo
                               const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// int8 [rows][K], boxes of `box` rows x 128 bytes, 128-byte swizzle
-int row_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int box)
+encode_fn encoder()
 {
     static encode_fn encode = [] {
         void *fn = nullptr;
@@ -529,6 +573,13 @@ int row_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int box
             fn = nullptr;
         return (encode_fn)fn;
     }();
+    return encode;
+}
+
+// int8 [rows][K], boxes of `box` rows x 128 bytes, 128-byte swizzle
+int row_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int box)
+{
+    encode_fn encode = encoder();
     if (!encode) return MAPLE_ERR_CUDA;
     cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)K};
@@ -536,6 +587,20 @@ int row_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int box
     const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, b, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MAPLE_OK : MAPLE_ERR_CUDA;
+}
+
+// y [T][N], boxes of 32 rows x 32 columns
+int out_map(CUtensorMap *map, void *y, int64_t T, int64_t N, bool bf16)
+{
+    encode_fn encode = encoder();
+    if (!encode) return MAPLE_ERR_CUDA;
+    cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)T};
+    cuuint64_t strides[1] = {(cuuint64_t)N * (bf16 ? 2 : 4)};
+    cuuint32_t b[2] = {32, 32}, estr[2] = {1, 1};
+    const CUresult r = encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, y, dims, strides, b, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? MAPLE_OK : MAPLE_ERR_CUDA;
 }
 
@@ -563,16 +628,20 @@ int launch_rows(const maple_attn_linear_args &a, const LinearOut &o, cudaStream_
     return cudaGetLastError() == cudaSuccess ? MAPLE_OK : MAPLE_ERR_CUDA;
 }
 
-// Tile width of the T > 128 form: rounds of the 148 SMs times the width (plus
-// what a tile costs whatever its width), the least over 64 .. 256
+// Tile width of the T > 128 form.  A step of 128 bytes of K writes (128 + bn) 128
+// bytes into shared memory and the products read as many, at 128 bytes a clock
+// together, which is more than the products' own 2 bn clocks: so the cost is the
+// rounds over the 148 SMs times 128 + bn, the least over widths 64 .. 256 (4096 x
+// 2560: 224 columns, 3 rounds).  Pairs of CTAs (256 x 256 tiles, each loading
+// half of B) moved a third less but took 30 us against 27: 160 tiles are three
+// rounds of 74 pairs.
 int pick_bn(int64_t T, int64_t N)
 {
     const int64_t ta = (T + 127) / 128;
     int best = 64;
     int64_t cost = -1;
     for (int bn = 64; bn <= 256; bn += 32) {
-        const int64_t rounds = (ta * ((N + bn - 1) / bn) + 147) / 148;
-        const int64_t c = rounds * (bn < 128 ? 64 + bn / 2 + 16 : bn + 16);   // (below 128 the 128-row operand's reads set the pace)
+        const int64_t rounds = (ta * ((N + bn - 1) / bn) + 147) / 148, c = rounds * (128 + bn);
         if (cost < 0 || c < cost || (c == cost && bn > best)) {
             cost = c;
             best = bn;
@@ -638,8 +707,13 @@ extern "C" int maple_attn_linear(const maple_attn_linear_args *args, maple_strea
     if (!rc) rc = row_map(&wm, a.w, a.N, K, swap ? 128 : p.bn);
     if (rc) return rc;
     const int stage = (128 + p.bn) * kGemmBK;
-    p.stages = 212992 / stage < 8 ? 212992 / stage : 8;
-    const int smem = p.stages * stage + 256;
+    const int room = swap ? 212992 : 212992 - 40960;
+    p.stages = room / stage < 8 ? room / stage : 8;
+    const int smem = p.stages * stage + (swap ? 0 : 40960) + 256;
+    const bool bf16 = a.y_dtype == MAPLE_BF16;
+    CUtensorMap ym = qm;       // (not read without y_tma)
+    p.y_tma = !swap && a.N % (bf16 ? 8 : 4) == 0;
+    if (p.y_tma && (rc = out_map(&ym, a.y, a.T, a.N, bf16))) return rc;
     auto kernel = swap ? linear_gemm_kernel<true> : linear_gemm_kernel<false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 216 * 1024) != cudaSuccess) {
         cudaGetLastError();
@@ -671,7 +745,7 @@ extern "C" int maple_attn_linear(const maple_attn_linear_args *args, maple_strea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    if (cudaLaunchKernelEx(&lc, kernel, swap ? wm : qm, swap ? qm : wm, p) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&lc, kernel, swap ? wm : qm, swap ? qm : wm, ym, p) != cudaSuccess) {
         cudaGetLastError();
         return MAPLE_ERR_CUDA;
     }

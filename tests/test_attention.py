@@ -43,7 +43,7 @@ def linear_ref(x, w, alpha, bias=None, resid=None):
 
 @pytest.mark.parametrize("T,K,N", [(1, 16, 1), (1, 2048, 2560), (2, 48, 7), (3, 272, 130), (8, 2048, 257), (16, 1040, 64), (17, 256, 333),
                                    (33, 4096, 40), (64, 512, 1000), (65, 128, 128), (130, 2048, 515), (257, 1040, 2560), (1000, 336, 96),
-                                   (5, 32768, 24), (300, 32768, 20)])
+                                   (5, 32768, 24), (300, 32768, 20), (2000, 1040, 4100), (4096, 512, 2560)])
 @pytest.mark.parametrize("dt", [BF16, FP32])
 def test_linear(T, K, N, dt):
     r = gen(T * 7 + K + N)
