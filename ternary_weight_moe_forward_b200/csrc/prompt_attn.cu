@@ -276,6 +276,14 @@ struct Range {
 
 constexpr int kItems = 2;   // items in hand: the one being worked on and the next
 
+// bit 15 of each half set where its exponent is all ones (an infinity or NaN); other bits mean nothing
+template <typename T>
+__device__ __forceinline__ uint32_t exponent_full(uint32_t w)
+{
+    constexpr bool B = __is_same(T, __nv_bfloat16);
+    return (w & (B ? 0x7f807f80u : 0x7c007c00u)) + (B ? 0x00800080u : 0x04000400u);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
@@ -576,27 +584,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < n; j++) {
                 const bool edge = g.masked(w, a.window, j);
-                if (edge && i == 0) {
-                    // V_j: what is not finite becomes 0 before the products read it
-                    const uint32_t t = t0 + j + 1;       // (V_j comes with K_j+1)
-                    if (!mbar_wait(b_full + 8 * (t % S), (t / S) & 1, abort, a.flags, limit)) ok = false;
-                    if (ok) {
-                        uint4 *tile = (uint4 *)(smem + L::kKv + ((t % S) * 2 + 1) * L::kTileBytes);
-                        bool any = false;
-#pragma unroll 4
-                        for (int c = threadIdx.x; c < L::kTileBytes / 16; c += 128) {
-                            const uint4 v = tile[c];
-                            const uint32_t e0 = not_finite<T>(v.x), e1 = not_finite<T>(v.y), e2 = not_finite<T>(v.z), e3 = not_finite<T>(v.w);
-                            if (e0 | e1 | e2 | e3) {
-                                tile[c] = make_uint4(v.x & ~e0, v.y & ~e1, v.z & ~e2, v.w & ~e3);
-                                any = true;
-                            }
-                        }
-                        if (any) atomicOr(odd_values + u % kItems, 1u);
-                        fence_async_smem();
-                        // (the products wait for all four warps' halves of P, so for all of the tile)
-                    }
-                }
                 ok = ok && mbar_wait(b_s + 8 * i, ns & 1, abort, a.flags, limit);
                 ok = __all_sync(FULL, ok);
                 if (!ok) break;
@@ -613,11 +600,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
 #pragma unroll
                     for (int c = 0; c < kKeys; c++) s[c] = -s[c];
                 }
-                if (edge) {
-                    const int base = g.kbeg + j * kKeys, hi = pos - base, lo = a.window ? pos - a.window + 1 - base : -1;
+                if (edge) {   // the columns lo .. hi as one bit each
+                    const int base = g.kbeg + j * kKeys, hi = pos - base, lo = a.window ? hi - a.window + 1 : 0;
 #pragma unroll
-                    for (int c = 0; c < kKeys; c++)
-                        if (c > hi || c < lo) s[c] = -INFINITY;
+                    for (int q = 0; q < kKeys; q += 32) {
+                        const int h = hi - q, l0 = lo - q;
+                        uint32_t keep = h >= 31 ? FULL : h < 0 ? 0u : (2u << h) - 1u;
+                        keep &= l0 <= 0 ? FULL : l0 > 31 ? 0u : FULL << l0;
+#pragma unroll
+                        for (int c = 0; c < 32; c++)
+                            if (!(keep & (1u << c))) s[q + c] = -INFINITY;
+                    }
                 }
                 float mx[4];
 #pragma unroll
@@ -666,6 +659,32 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     tmem_st32(tp + c / 2, pk);
                 }
                 tmem_wait_st();
+                if (edge && i == 0) {
+                    // V_j: what is not finite becomes 0 before the products read it (they wait for P of all
+                    // four warps, so for all of the tile)
+                    const uint32_t t = t0 + j + 1;       // (V_j comes with K_j+1)
+                    if (!mbar_wait(b_full + 8 * (t % S), (t / S) & 1, abort, a.flags, limit)) ok = false;
+                    uint4 *tile = (uint4 *)(smem + L::kKv + ((t % S) * 2 + 1) * L::kTileBytes);
+                    constexpr int N16 = L::kTileBytes / 16 / 128;
+                    uint32_t found = 0;
+                    if (ok) {
+#pragma unroll 2
+                        for (int c = 0; c < N16; c++) {
+                            const uint4 v = tile[threadIdx.x + 128 * c];
+                            found |= exponent_full<T>(v.x) | exponent_full<T>(v.y) | exponent_full<T>(v.z) | exponent_full<T>(v.w);
+                        }
+                    }
+                    if (found & 0x80008000u) {
+                        for (int c = 0; c < N16; c++) {
+                            const uint4 v = tile[threadIdx.x + 128 * c];
+                            tile[threadIdx.x + 128 * c] = make_uint4(v.x & ~not_finite<T>(v.x), v.y & ~not_finite<T>(v.y),
+                                                                     v.z & ~not_finite<T>(v.z), v.w & ~not_finite<T>(v.w));
+                        }
+                        atomicOr(odd_values + u % kItems, 1u);
+                        fence_async_smem();
+                    }
+                    if (!__all_sync(FULL, ok)) break;
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_p + 8 * i);
