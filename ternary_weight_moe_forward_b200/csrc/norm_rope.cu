@@ -30,7 +30,7 @@ bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 // took 66 us for 16384 tokens of 36 heads of 64.
 constexpr int kRopeWarps = 4, kAhead = 2;
 
-template <typename T, int D>
+template <typename T, int D, bool INTER, bool CACHE>
 __global__ void __launch_bounds__(kRopeWarps * 32, 8) qk_norm_rope_kernel(const maple_attn_rope_args a, const int parts)
 {
     using P = KvPage<D>;
@@ -39,19 +39,18 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 8) qk_norm_rope_kernel(const 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPH;
     float *cs = s_angle[warp][0], *sn = s_angle[warp][1];
     const int H = a.heads, Hkv = a.kv_heads, rd = a.rotary_dim, half = rd >> 1;
-    const int U = H + Hkv + (a.pages ? Hkv : 0), steps = (U + HPW - 1) / HPW;
+    const int U = H + Hkv + (CACHE ? Hkv : 0), steps = (U + HPW - 1) / HPW;
     const int n = a.page_size;
     const int64_t jobs = a.T * parts, nw = (int64_t)gridDim.x * kRopeWarps;
 
   for (int64_t job = blockIdx.x * (int64_t)kRopeWarps + warp; job < jobs; job += nw) {
     const int64_t t = job / parts;
     const int part = (int)(job - t * parts);
-    auto source = [&](int u) {
-        const T *p = u < H         ? (const T *)a.q + t * a.q_stride + (int64_t)u * D
-                     : u < H + Hkv ? (const T *)a.k + t * a.k_stride + (int64_t)(u - H) * D
-                                   : (const T *)a.v + t * a.v_stride + (int64_t)(u - H - Hkv) * D;
-        return reinterpret_cast<const uint4 *>(p) + l;
-    };
+    // head u of q, k and v is at base + u D
+    const T *bq = (const T *)a.q + t * a.q_stride + 8 * l;
+    const T *bk = (const T *)a.k + t * a.k_stride + 8 * l - (int64_t)H * D;
+    const T *bv = CACHE ? (const T *)a.v + t * a.v_stride + 8 * l - (int64_t)(H + Hkv) * D : bk;
+    auto source = [&](int u) { return reinterpret_cast<const uint4 *>((u < H ? bq : u < H + Hkv ? bk : bv) + u * D); };
     uint4 ahead[kAhead];
     auto load = [&](int s0) {
 #pragma unroll
@@ -62,7 +61,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 8) qk_norm_rope_kernel(const 
     };
     load(part);
     int64_t slot = -1;
-    if (a.pages) {
+    if (CACHE) {
         slot = __ldg(a.slots + t);
         if (slot >= a.num_pages * n) {
             if (lane == 0) set_flag(a.flags, MAPLE_DEVFLAG_BAD_INDEX);
@@ -115,7 +114,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 8) qk_norm_rope_kernel(const 
         }
         // ---- rotation
         const int c0 = 8 * l;
-        if (a.interleaved) {
+        if (INTER) {
             if (qk && c0 < rd) {
                 const float4 c4 = reinterpret_cast<const float4 *>(cs)[l], s4 = reinterpret_cast<const float4 *>(sn)[l];
                 const float cv[4] = {c4.x, c4.y, c4.z, c4.w}, sv[4] = {s4.x, s4.y, s4.z, s4.w};
@@ -148,7 +147,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 8) qk_norm_rope_kernel(const 
         const uint4 out = pack8<T>(x);
         if (on && u < H) reinterpret_cast<uint4 *>((T *)a.q_out + (t * H + u) * D)[l] = out;
         else if (on && qk && a.k_out) reinterpret_cast<uint4 *>((T *)a.k_out + (t * Hkv + (u - H)) * D)[l] = out;
-        if (!__any_sync(FULL, on && u >= H && slot >= 0)) continue;
+        if (!CACHE || !__any_sync(FULL, on && u >= H && slot >= 0)) continue;
         // ---- 4-bit codes of the keys (as rounded) and values
         unpack8<T>(out, x);   // (a value is its own rounding)
         float lo = kKvClamp, hi = -kKvClamp;
@@ -237,6 +236,11 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const maple_attn_read_args
     }
 }
 
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
+
 bool heads_ok(int H, int Hkv) { return H >= 1 && Hkv >= 1 && H <= 1024 && H % Hkv == 0; }
 
 }  // namespace
@@ -277,12 +281,19 @@ extern "C" int maple_attn_qk_norm_rope(const maple_attn_rope_args *args, maple_s
     const unsigned grid = (unsigned)(blocks < 148 * 16 ? blocks : 148 * 16);
     const int threads = kRopeWarps * 32;
     cudaStream_t st = (cudaStream_t)stream;
+    auto launch = [&](auto elem, auto dim) {
+        using T = decltype(elem);
+        constexpr int DIM = decltype(dim)::value;
+        auto kernel = a.interleaved ? (a.pages ? qk_norm_rope_kernel<T, DIM, true, true> : qk_norm_rope_kernel<T, DIM, true, false>)
+                                    : (a.pages ? qk_norm_rope_kernel<T, DIM, false, true> : qk_norm_rope_kernel<T, DIM, false, false>);
+        kernel<<<grid, threads, 0, st>>>(a, parts);
+    };
     if (a.dtype == MAPLE_BF16) {
-        if (D == 128) qk_norm_rope_kernel<__nv_bfloat16, 128><<<grid, threads, 0, st>>>(a, parts);
-        else qk_norm_rope_kernel<__nv_bfloat16, 64><<<grid, threads, 0, st>>>(a, parts);
+        if (D == 128) launch(__nv_bfloat16(), Int<128>());
+        else launch(__nv_bfloat16(), Int<64>());
     } else {
-        if (D == 128) qk_norm_rope_kernel<__half, 128><<<grid, threads, 0, st>>>(a, parts);
-        else qk_norm_rope_kernel<__half, 64><<<grid, threads, 0, st>>>(a, parts);
+        if (D == 128) launch(__half(), Int<128>());
+        else launch(__half(), Int<64>());
     }
     return cudaGetLastError() == cudaSuccess ? MAPLE_OK : MAPLE_ERR_CUDA;
 }
