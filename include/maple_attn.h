@@ -27,8 +27,8 @@
  * Head layout: `heads` query heads in `kv_heads` groups of heads/kv_heads;
  * query head h reads key/value head h / (heads/kv_heads).  head_dim is 64 or
  * 128.  A token's heads are contiguous; the step from token to token is a
- * stride in elements (a multiple of 8), so views of one fused projection are
- * taken as they are.
+ * stride in elements (a multiple of 8; positive in maple_attn_prompt), so views
+ * of one fused projection are taken as they are.
  */
 #ifndef MAPLE_ATTN_H
 #define MAPLE_ATTN_H
@@ -75,7 +75,9 @@ int64_t maple_attn_page_bytes(int32_t head_dim, int32_t page_size);
  * are those of the expert matrices, and the sum is exact.
  * normalise != 0: x is the fp32 residual stream and the row that is quantised
  * is bf16(RMSNorm(x)) (norm weights 1, eps 1e-6, the layer stack's rule; K must
- * be a multiple of 256 then).  resid may be y.
+ * be a multiple of 256 then).
+ * resid may be y; y overlaps nothing else that the call reads (with normalise
+ * it may be x too).
  * Limits: K a multiple of 16, 16 <= K <= 32768; 1 <= N; T*N and N*K < 2^40.
  * T == 0 is a no-op.
  */

@@ -7,9 +7,9 @@
     cached_attention   attention of one new token per sequence over the cache
 
 Each function checks its tensors, allocates outputs and scratch with torch on
-the tensors' device and launches on that device's current stream (or `stream`);
-none synchronises, and all may be captured into a CUDA graph.  A tensor of the
-wrong type, shape, stride or device raises ValueError, an error of the library
+the tensors' device and launches on that device's current stream; none
+synchronises, and all may be captured into a CUDA graph.  A tensor of the wrong
+type, shape, stride or device raises ValueError, an error of the library
 MapleError.  What only the kernels can see (a page number outside the cache) is
 reported in `flags`, an int32 tensor of one element that the caller zeroes and
 reads (MAPLE_FLAG_* bits).  No gradients: these are serving operators.
@@ -65,12 +65,11 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _call(name: str, args: bytes, dev: int, stream) -> None:
-    """Launch on `stream` or the device's current one, with that device current."""
+def _call(name: str, args: bytes, dev: int) -> None:
+    """Launch on the device's current stream, with that device current."""
     if _fn is None:
         _lib()
-    if stream is None:
-        stream = _raw_stream(dev)
+    stream = _raw_stream(dev)
     if dev == _current_device():
         rc = _calls[name](args, stream)
     else:
@@ -146,7 +145,7 @@ def _page_size(pages, kv_heads: int, head_dim: int) -> int:
 
 def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias: torch.Tensor | None = None,
                 resid: torch.Tensor | None = None, normalise: bool = False, out_dtype: torch.dtype = torch.float32,
-                out: torch.Tensor | None = None, flags: torch.Tensor | None = None, stream: int | None = None) -> torch.Tensor:
+                out: torch.Tensor | None = None, flags: torch.Tensor | None = None) -> torch.Tensor:
     """y = (q_x weight^T) * (s_x alpha) (+ bias) (+ resid), q_x and s_x the int8 absmax codes and scales of x's rows.
 
     x bf16 [T][K] (rows may be strided), or the fp32 residual stream with `normalise` (its RMS-normed rows, rounded to
@@ -177,14 +176,14 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias
     _call("linear", _LINEAR.pack(
         x.data_ptr(), weight.data_ptr(), _vector(alpha, torch.float32, N, "alpha must be fp32 [N]"),
         _vector(bias, torch.float32, N, "bias must be fp32 [N]"), 0 if resid is None else resid.data_ptr(), out.data_ptr(),
-        0 if ws is None else ws.data_ptr(), n, _flags(flags), x.stride(0) if T > 1 else K, T, K, N, ydt, 1 if normalise else 0), dev, stream)
+        0 if ws is None else ws.data_ptr(), n, _flags(flags), x.stride(0) if T > 1 else K, T, K, N, ydt, 1 if normalise else 0), dev)
     return out
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
                  q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
                  interleaved: bool = False, v: torch.Tensor | None = None, pages: torch.Tensor | None = None,
-                 slots: torch.Tensor | None = None, flags: torch.Tensor | None = None, stream: int | None = None):
+                 slots: torch.Tensor | None = None, flags: torch.Tensor | None = None):
     """(q', k'): every head normed (RMS, weights fp32 [head_dim] or 1) and rotated by its position.
 
     q [T][heads][d], k [T][kv_heads][d], bf16 or fp16 (views of one projection are taken as they are); positions int64
@@ -219,12 +218,12 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_
         _vector(positions, torch.int64, T, "positions must be int64 [T]"),
         _vector(inv_freq, torch.float64, rot, "inv_freq must be float64 [rotary_dim/2]"), pp,
         _vector(slots, torch.int64, T, "slots must be int64 [T]"), _flags(flags), qs, ks, vs, T, P, H, Hkv, d, 2 * rot, n,
-        _HEAD_TYPES[dt], 1 if interleaved else 0, eps), dev, stream)
+        _HEAD_TYPES[dt], 1 if interleaved else 0, eps), dev)
     return qo, ko
 
 
 def kv_read(pages: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: torch.dtype = torch.bfloat16,
-            flags: torch.Tensor | None = None, stream: int | None = None):
+            flags: torch.Tensor | None = None):
     """(k, v) [n][kv_heads][head_dim]: the values that the cache holds at `slots` (int64 [n]; < 0 reads as zeros)."""
     if dtype not in _HEAD_TYPES:
         raise ValueError("dtype must be bf16 or fp16")
@@ -237,13 +236,13 @@ def kv_read(pages: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: torc
     k = pages.new_empty((n, Hkv, head_dim), dtype=dtype)
     v = torch.empty_like(k)
     _call("kv_read", _READ.pack(pages.data_ptr(), _vector(slots, torch.int64, n, "slots must be int64 [n]"), k.data_ptr(),
-                                v.data_ptr(), _flags(flags), n, P, Hkv, head_dim, page_size, _HEAD_TYPES[dtype]), dev, stream)
+                                v.data_ptr(), _flags(flags), n, P, Hkv, head_dim, page_size, _HEAD_TYPES[dtype]), dev)
     return k, v
 
 
 def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
                      max_q: int, scale: float | None = None, window: int = 0, return_lse: bool = False,
-                     out: torch.Tensor | None = None, flags: torch.Tensor | None = None, stream: int | None = None):
+                     out: torch.Tensor | None = None, flags: torch.Tensor | None = None):
     """Causal attention over packed sequences: out [Tq][heads][d] (and lse fp32 [Tq][heads]).
 
     q [Tq][heads][d], k and v [Tk][kv_heads][d], bf16 or fp16; cu_q, cu_k int32 [B+1], the rows where sequences begin;
@@ -272,13 +271,12 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
         _vector(cu_q, torch.int32, B + 1, "cu_q must be int32 [B+1]"), _vector(cu_k, torch.int32, B + 1, "cu_k must be int32 [B+1]"),
         _flags(flags), qs, ks, vs, Tq, Tk, B, max_q, H, Hkv, d, window, _HEAD_TYPES[dt], d ** -0.5 if scale is None else scale),
-        dev, stream)
+        dev)
     return (out, lse) if return_lse else out
 
 
 def cached_attention(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
-                     scale: float | None = None, window: int = 0, flags: torch.Tensor | None = None,
-                     stream: int | None = None) -> torch.Tensor:
+                     scale: float | None = None, window: int = 0, flags: torch.Tensor | None = None) -> torch.Tensor:
     """Attention of one new token per sequence over its cached tokens: out [B][heads][d].
 
     q [B][heads][d] bf16 or fp16; block_table int32 [B][max_pages]; lens int32 [B], the cached tokens of each sequence
@@ -303,5 +301,5 @@ def cached_attention(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Te
     _call("cached", _CACHED.pack(
         q.data_ptr(), out.data_ptr(), pages.data_ptr(), block_table.data_ptr(), _vector(lens, torch.int32, B, "lens must be int32 [B]"),
         0 if ws is None else ws.data_ptr(), w, _flags(flags), qs, block_table.stride(0) if B > 1 else mp, P, B, mp, H, Hkv, d, n, window,
-        _HEAD_TYPES[dt], d ** -0.5 if scale is None else scale), dev, stream)
+        _HEAD_TYPES[dt], d ** -0.5 if scale is None else scale), dev)
     return out

@@ -206,46 +206,52 @@ struct Item {
 
 // The item of a block: (sequence, pair) in the order of the sequences from the
 // last one, a sequence's pairs from its last tokens, key/value heads fastest.
-// One warp; 32 sequences at a time.  kvh = -2: beyond the last item.
+// One warp; 256 sequences at a time, 8 per lane.  kvh = -2: beyond the last item.
 __device__ __forceinline__ Item find_item(const maple_attn_prompt_args &a, int nt, int block)
 {
     const int lane = threadIdx.x & 31, span = 2 * nt;
     Item it;
     it.kvh = -2;
     const int x = block / a.kv_heads;
+    auto rows = [&](int b, int64_t &q0, int64_t &q1) {      // query rows, as cut to Tq
+        q0 = min(max((int64_t)__ldg(a.cu_q + b), (int64_t)0), a.Tq);
+        q1 = min(max((int64_t)__ldg(a.cu_q + b + 1), q0), a.Tq);
+    };
+    auto pairs = [&](int b) {
+        int64_t q0, q1;
+        rows(b, q0, q1);
+        return (int)((min(q1 - q0, (int64_t)a.max_q) + span - 1) / span);
+    };
     int at = 0;
-    for (int b0 = a.B - 1; b0 >= 0; b0 -= 32) {
-        const int b = b0 - lane;
-        int n = 0;
-        int64_t q0 = 0, q1 = 0, qfull = 0;
-        if (b >= 0) {
-            const int64_t u = __ldg(a.cu_q + b), v = __ldg(a.cu_q + b + 1);
-            q0 = min(max(u, (int64_t)0), a.Tq);
-            qfull = q1 = min(max(v, q0), a.Tq);
-            q1 = min(q1, q0 + a.max_q);
-            n = (int)((q1 - q0 + span - 1) / span);
-        }
-        int inc = n;
+    for (int b0 = a.B - 1; b0 >= 0; b0 -= 256) {
+        int sum = 0;
+#pragma unroll 2
+        for (int i = 0; i < 8; i++)
+            if (b0 - lane * 8 - i >= 0) sum += pairs(b0 - lane * 8 - i);
+        int inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(FULL, inc, o);
             if (lane >= o) inc += v;
         }
-        const int from = at + inc - n;
-        const unsigned hit = __ballot_sync(FULL, x >= from && x < from + n);
+        const unsigned hit = __ballot_sync(FULL, x >= at + inc - sum && x < at + inc);
         if (hit) {
-            int64_t k0 = 0, k1 = 0;
-            if (b >= 0) {
-                k0 = min(max((int64_t)__ldg(a.cu_k + b), (int64_t)0), a.Tk);
-                k1 = min(max((int64_t)__ldg(a.cu_k + b + 1), k0), a.Tk);
-            }
             const int src = __ffs(hit) - 1;
+            int b = b0 - src * 8, rest = x - __shfl_sync(FULL, at + inc - sum, src), n;
+            while (rest >= (n = pairs(b))) {
+                rest -= n;
+                b--;
+            }
+            int64_t q0, q1;
+            rows(b, q0, q1);
+            const int64_t k0 = min(max((int64_t)__ldg(a.cu_k + b), (int64_t)0), a.Tk);
+            const int64_t k1 = min(max((int64_t)__ldg(a.cu_k + b + 1), k0), a.Tk);
             it.kvh = block - x * a.kv_heads;
-            it.tA = __shfl_sync(FULL, (n - 1 - (x - from)) * span, src);
-            it.q0 = __shfl_sync(FULL, (int)q0, src);
-            it.lq = __shfl_sync(FULL, (int)(q1 - q0), src);
-            it.k0 = __shfl_sync(FULL, (int)k0, src);
-            it.off = __shfl_sync(FULL, (int)((k1 - k0) - (qfull - q0)), src);   // (a cut by max_q moves no position)
+            it.tA = (n - 1 - rest) * span;
+            it.q0 = (int)q0;
+            it.lq = (int)min(q1 - q0, (int64_t)a.max_q);
+            it.k0 = (int)k0;
+            it.off = (int)((k1 - k0) - (q1 - q0));   // (a cut by max_q moves no position)
             return it;
         }
         at += __shfl_sync(FULL, inc, 31);
@@ -811,7 +817,7 @@ extern "C" int maple_attn_prompt(const maple_attn_prompt_args *args, maple_strea
     for (const void *p : {(const void *)a.cu_q, (const void *)a.cu_k, (const void *)a.lse})
         if ((uintptr_t)p & 3u) return MAPLE_ERR_INVALID_ARG;
     for (int64_t s : {a.q_stride, a.k_stride, a.v_stride})
-        if (s % 8 || s < 0 || s >= (1ll << 38)) return MAPLE_ERR_INVALID_ARG;
+        if (s % 8 || s <= 0 || s >= (1ll << 38)) return MAPLE_ERR_INVALID_ARG;
     PromptK k;
     k.a = a;
     k.G = a.heads / a.kv_heads;

@@ -298,6 +298,36 @@ def test_prompt_what_is_masked_does_not_reach(window, dt):
     assert torch.equal(g1[~s3][..., 3], b1[~s3][..., 3]) and torch.equal(g1[~s5][..., 5], b1[~s5][..., 5])
 
 
+def test_prompt_many_short_sequences_and_none():
+    """700 sequences of 0 to 5 tokens (more than one round of the search for a block's sequence); no keys at all."""
+    lens = [(i * 7) % 6 for i in range(700)]
+    r = gen(17)
+    H, Hkv, d, n = 4, 2, 64, sum(lens)
+    q, k, v = r(n, H, d).to(FP16), r(n, Hkv, d).to(FP16), r(n, Hkv, d).to(FP16)
+    out, lse = tw.prompt_attention(q, k, v, cu(lens), cu(lens), 5, return_lse=True)
+    check_prompt(out, lse, *ref.prompt(q, k, v, lens, lens, d ** -0.5, 0), FP16)
+    out, lse = tw.prompt_attention(q[:40], k[:0], v[:0], cu([40]), cu([0]), 40, return_lse=True)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    assert tw.prompt_attention(q[:0], k, v, cu([0]), cu([n]), 0).shape == (0, H, d)
+
+
+def test_prompt_nan_among_the_keys_that_are_seen():
+    """A NaN key makes the rows that see it NaN, an infinite one too, wherever it stands in a tile of 128 keys."""
+    r = gen(19)
+    d, n = 128, 300
+    q, k, v = r(n, 2, d).to(BF16), r(n, 1, d).to(BF16), r(n, 1, d).to(BF16)
+    base = tw.prompt_attention(q, k, v, cu([n]), cu([n]), n)
+    for j in (0, 5, 64, 127, 128, 299):
+        for bad in (math.nan, math.inf):
+            k2 = k.clone()
+            k2[j, 0, 7] = bad
+            got = tw.prompt_attention(q, k2, v, cu([n]), cu([n]), n)
+            assert torch.equal(got[:j], base[:j])
+            hit = q[j:, :, 7].float() * bad
+            gone = hit.isnan() | (hit == math.inf)           # (a score of -inf is a weight of 0)
+            assert got[j:][gone].isnan().all()
+
+
 def test_prompt_bad_offsets_are_cut_and_flagged():
     r = gen(15)
     d = 64
@@ -387,6 +417,26 @@ def test_cached_query_magnitudes():
         check_cached(out, q, kv, lens, 0.09 / size, 0, BF16)
     out = tw.cached_attention(torch.zeros_like(q), pages, table, ln)
     check_cached(out, torch.zeros_like(q), kv, lens, d ** -0.5, 0, BF16)
+
+
+def test_cached_nan_values_stay_in_their_channels():
+    """A NaN key's token makes its sequence's rows NaN; a NaN value its own 32 channels; other sequences are untouched."""
+    r = gen(29)
+    d, n, lens = 128, 16, [50, 90]
+    pages, table, kv = make_cache(r, lens, 1, d, n)
+    q, ln = r(2, 4, d).to(BF16), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    base = tw.cached_attention(q, pages, table, ln)
+    k = kv[0][0][20:21].float().to(BF16)
+    vbad = kv[0][1][20:21].float().to(BF16)
+    vbad[0, 0, 70] = math.nan
+    slot = (table[0, 1].long() * n + 4)[None]
+    ref.fill_pages(pages, n, k, torch.nan_to_num(vbad), slot)
+    tw.qk_norm_rope(k, k, slot * 0, freqs(0), v=vbad, pages=pages, slots=slot)
+    got = tw.cached_attention(q, pages, table, ln)
+    assert torch.equal(got[1], base[1])
+    assert got[0, :, 64:96].isnan().all() and got[0, :, :64].isfinite().all() and got[0, :, 96:].isfinite().all()
+    window = tw.cached_attention(q, pages, table, ln, window=25)       # the NaN row is masked, in a tile that is read
+    assert window.isfinite().all()
 
 
 def test_cached_bad_pages_and_lengths():

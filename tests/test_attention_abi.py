@@ -95,7 +95,8 @@ BAD, SHAPE = tw.MAPLE_ERR_INVALID_ARG, tw.MAPLE_ERR_UNSUPPORTED_SHAPE
     *[("read", READ, c, SHAPE) for c in (dict(d=32), dict(ps=8), dict(Hkv=0))],
     *[("prompt", PROMPT, c, BAD) for c in (dict(q=0), dict(k=0), dict(v=0), dict(out=0), dict(cq=0), dict(ck=0), dict(B=-1), dict(mq=-1),
                                            dict(win=-1), dict(Tq=-1), dict(dt=2), dict(scale=float("inf")), dict(qs=513),
-                                           dict(out=P + 8), dict(cq=P + 2), dict(B=1 << 17))],
+                                           dict(out=P + 8), dict(cq=P + 2), dict(B=1 << 17), dict(ks=0), dict(vs=-256),
+                                           dict(Tk=1 << 31))],
     *[("prompt", PROMPT, c, SHAPE) for c in (dict(d=256), dict(H=5), dict(H=0), dict(Hkv=0), dict(H=256, Hkv=2))],
     *[("cached", CACHED, c, BAD) for c in (dict(q=0), dict(out=0), dict(pages=0), dict(bt=0), dict(lens=0), dict(NP=0), dict(B=-1),
                                            dict(mp=-1), dict(win=-1), dict(dt=2), dict(scale=float("nan")), dict(q=P + 8),
