@@ -206,7 +206,8 @@ struct Item {
 
 // The item of a block: (sequence, pair) in the order of the sequences from the
 // last one, a sequence's pairs from its last tokens, key/value heads fastest.
-// One warp; 256 sequences at a time, 8 per lane.  kvh = -2: beyond the last item.
+// One warp; 32 sequences at a time, or 256 (8 per lane) where there are more than
+// 32.  kvh = -2: beyond the last item.
 __device__ __forceinline__ Item find_item(const maple_attn_prompt_args &a, int nt, int block)
 {
     const int lane = threadIdx.x & 31, span = 2 * nt;
@@ -222,12 +223,12 @@ __device__ __forceinline__ Item find_item(const maple_attn_prompt_args &a, int n
         rows(b, q0, q1);
         return (int)((min(q1 - q0, (int64_t)a.max_q) + span - 1) / span);
     };
+    const int per = a.B > 32 ? 8 : 1;
     int at = 0;
-    for (int b0 = a.B - 1; b0 >= 0; b0 -= 256) {
+    for (int b0 = a.B - 1; b0 >= 0; b0 -= 32 * per) {
         int sum = 0;
-#pragma unroll 2
-        for (int i = 0; i < 8; i++)
-            if (b0 - lane * 8 - i >= 0) sum += pairs(b0 - lane * 8 - i);
+        for (int i = 0; i < per; i++)
+            if (b0 - lane * per - i >= 0) sum += pairs(b0 - lane * per - i);
         int inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -237,7 +238,7 @@ __device__ __forceinline__ Item find_item(const maple_attn_prompt_args &a, int n
         const unsigned hit = __ballot_sync(FULL, x >= at + inc - sum && x < at + inc);
         if (hit) {
             const int src = __ffs(hit) - 1;
-            int b = b0 - src * 8, rest = x - __shfl_sync(FULL, at + inc - sum, src), n;
+            int b = b0 - src * per, rest = x - __shfl_sync(FULL, at + inc - sum, src), n;
             while (rest >= (n = pairs(b))) {
                 rest -= n;
                 b--;
