@@ -40,7 +40,8 @@ _CACHED = struct.Struct("=6Q q Q 3q 8i f 4x")
 
 _fn = None
 _calls = {}     # the entry points by name
-_UNIT = (1,)
+_PAGE_SIZES = (16, 32, 64)
+_CONTIGUOUS = torch.contiguous_format
 
 
 def _lib():
@@ -108,9 +109,7 @@ def _vector(t, dtype, n: int, what: str) -> int:
     """Address of a contiguous vector of n values (0 for None)."""
     if t is None:
         return 0
-    if t.dtype is dtype and t.stride() == _UNIT and t.shape[0] == n:
-        return t.data_ptr()
-    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != n or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(what)
     return t.data_ptr()
 
@@ -120,10 +119,10 @@ def _heads(t, dtype, what: str):
     if t.dim() != 3 or t.dtype is not dtype:
         raise ValueError(what)
     n, h, d = t.shape
-    s = t.stride()
-    if s[2] != 1 or (s[1] != d and h != 1):
+    step, head, one = t.stride()
+    if one != 1 or (head != d and h != 1):
         raise ValueError(what)
-    return n, h, d, (s[0] if n > 1 else h * d)
+    return n, h, d, (step if n > 1 else h * d)
 
 
 def kv_pages(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, device="cuda") -> torch.Tensor:
@@ -132,15 +131,15 @@ def kv_pages(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, 
     return torch.zeros(num_pages, kv_heads, b, dtype=torch.uint8, device=device)
 
 
-def _page_size(pages, kv_heads: int, head_dim: int) -> int:
+def _pages(pages, head_dim: int):
+    """(num_pages, kv_heads, page_size) of a cache tensor."""
     if pages.dtype is not torch.uint8 or pages.dim() != 3 or not pages.is_contiguous():
         raise ValueError("pages must be a contiguous uint8 [num_pages][kv_heads][page bytes]")
-    if pages.shape[1] != kv_heads:
-        raise ValueError("the cache holds another number of key/value heads")
-    n, rest = divmod(pages.shape[2] * 4, 5 * head_dim)
-    if rest or n not in (16, 32, 64):
+    P, Hkv, size = pages.shape
+    n = 4 * size // (5 * head_dim)
+    if 4 * size != 5 * head_dim * n or n not in _PAGE_SIZES:
         raise ValueError("the pages do not fit this head_dim")
-    return n
+    return P, Hkv, n
 
 
 def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias: torch.Tensor | None = None,
@@ -151,14 +150,17 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias
     x bf16 [T][K] (rows may be strided), or the fp32 residual stream with `normalise` (its RMS-normed rows, rounded to
     bf16, are quantised).  weight int8 [N][K], alpha fp32 [N], bias fp32 [N], resid fp32 [T][N] (may be `out`).
     """
-    if x.dim() != 2 or weight.dim() != 2 or x.shape[1] != weight.shape[1]:
+    if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("x must be [T][K] and weight [N][K]")
     T, K = x.shape
-    N = weight.shape[0]
+    N, Kw = weight.shape
+    if K != Kw:
+        raise ValueError("x must be [T][K] and weight [N][K]")
+    step, one = x.stride()
     dev = _device(x, weight, alpha, bias, resid, out, flags)
     if x.dtype is not (torch.float32 if normalise else torch.bfloat16):
         raise ValueError("x must be bf16, or fp32 with normalise")
-    if x.stride(1) != 1 and K != 1:
+    if one != 1 and K != 1:
         raise ValueError("the rows of x must be contiguous")
     if weight.dtype is not torch.int8 or not weight.is_contiguous():
         raise ValueError("weight must be contiguous int8")
@@ -176,7 +178,7 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias
     _call("linear", _LINEAR.pack(
         x.data_ptr(), weight.data_ptr(), _vector(alpha, torch.float32, N, "alpha must be fp32 [N]"),
         _vector(bias, torch.float32, N, "bias must be fp32 [N]"), 0 if resid is None else resid.data_ptr(), out.data_ptr(),
-        0 if ws is None else ws.data_ptr(), n, _flags(flags), x.stride(0) if T > 1 else K, T, K, N, ydt, 1 if normalise else 0), dev)
+        0 if ws is None else ws.data_ptr(), n, _flags(flags), step if T > 1 else K, T, K, N, ydt, 1 if normalise else 0), dev)
     return out
 
 
@@ -203,13 +205,14 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_
         if v is None or slots is None:
             raise ValueError("pages, v and slots go together")
         vs = _heads(v, dt, "v must be [T][kv_heads][d] of q's type, a token's heads contiguous")[3]
-        if v.shape != k.shape:
-            raise ValueError("v must have the shape of k")
-        n, P, vp, pp = _page_size(pages, Hkv, d), pages.shape[0], v.data_ptr(), pages.data_ptr()
+        P, Hc, n = _pages(pages, d)
+        if v.shape != k.shape or Hc != Hkv:
+            raise ValueError("v must have the shape of k, and the cache its heads")
+        vp, pp = v.data_ptr(), pages.data_ptr()
     elif v is not None or slots is not None:
         raise ValueError("pages, v and slots go together")
-    qo = q.new_empty((T, H, d))
-    ko = q.new_empty((T, Hkv, d))
+    qo = torch.empty_like(q, memory_format=_CONTIGUOUS)
+    ko = torch.empty_like(k, memory_format=_CONTIGUOUS)
     rot = inv_freq.shape[0]
     _call("qk_norm_rope", _ROPE.pack(
         q.data_ptr(), k.data_ptr(), vp, qo.data_ptr(), ko.data_ptr(),
@@ -227,12 +230,9 @@ def kv_read(pages: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: torc
     """(k, v) [n][kv_heads][head_dim]: the values that the cache holds at `slots` (int64 [n]; < 0 reads as zeros)."""
     if dtype not in _HEAD_TYPES:
         raise ValueError("dtype must be bf16 or fp16")
-    if pages.dim() != 3 or slots.dim() != 1:
-        raise ValueError("pages must be [num_pages][kv_heads][page bytes] and slots [n]")
-    P, Hkv = pages.shape[0], pages.shape[1]
-    page_size = _page_size(pages, Hkv, head_dim)
+    P, Hkv, page_size = _pages(pages, head_dim)
     dev = _device(pages, slots, flags)
-    n = slots.shape[0]
+    n = slots.numel()
     k = pages.new_empty((n, Hkv, head_dim), dtype=dtype)
     v = torch.empty_like(k)
     _call("kv_read", _READ.pack(pages.data_ptr(), _vector(slots, torch.int64, n, "slots must be int64 [n]"), k.data_ptr(),
@@ -259,11 +259,11 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     if k.shape != v.shape or dk != d:
         raise ValueError("k and v must have one shape and q's head_dim")
     dev = _device(q, k, v, cu_q, cu_k, out, flags)
-    B = cu_q.shape[0] - 1
+    B = cu_q.numel() - 1
     if B < 0:
         raise ValueError("cu_q must be int32 [B+1]")
     if out is None:
-        out = q.new_empty((Tq, H, d))
+        out = torch.empty_like(q, memory_format=_CONTIGUOUS)
     elif out.dtype is not dt or out.shape != (Tq, H, d) or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's type and shape")
     lse = q.new_empty((Tq, H), dtype=torch.float32) if return_lse else None
@@ -286,20 +286,19 @@ def cached_attention(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Te
     if dt not in _HEAD_TYPES:
         raise ValueError("q must be bf16 or fp16")
     B, H, d, qs = _heads(q, dt, "q must be [B][heads][d], a token's heads contiguous")
-    if pages.dim() != 3:
-        raise ValueError("pages must be [num_pages][kv_heads][page bytes]")
-    P, Hkv = pages.shape[0], pages.shape[1]
-    n = _page_size(pages, Hkv, d)
+    P, Hkv, n = _pages(pages, d)
     dev = _device(q, pages, block_table, lens, flags)
-    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B or (
-            block_table.stride(1) != 1 and block_table.shape[1] > 1):
+    if block_table.dtype is not torch.int32 or block_table.dim() != 2:
         raise ValueError("block_table must be int32 [B][max_pages]")
-    mp = block_table.shape[1]
-    out = q.new_empty((B, H, d))
+    rows, mp = block_table.shape
+    step, one = block_table.stride()
+    if rows != B or (one != 1 and mp > 1):
+        raise ValueError("block_table must be int32 [B][max_pages]")
+    out = torch.empty_like(q, memory_format=_CONTIGUOUS)
     w = _size((_fn or _lib()).maple_attn_cached_workspace(B, mp, H, Hkv, d, n, window), "maple_attn_cached")
     ws = q.new_empty(w, dtype=torch.uint8) if w else None
     _call("cached", _CACHED.pack(
         q.data_ptr(), out.data_ptr(), pages.data_ptr(), block_table.data_ptr(), _vector(lens, torch.int32, B, "lens must be int32 [B]"),
-        0 if ws is None else ws.data_ptr(), w, _flags(flags), qs, block_table.stride(0) if B > 1 else mp, P, B, mp, H, Hkv, d, n, window,
+        0 if ws is None else ws.data_ptr(), w, _flags(flags), qs, step if B > 1 else mp, P, B, mp, H, Hkv, d, n, window,
         _HEAD_TYPES[dt], d ** -0.5 if scale is None else scale), dev)
     return out

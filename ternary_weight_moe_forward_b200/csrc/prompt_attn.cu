@@ -363,12 +363,16 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       if (warp == 10) {
         // ---------------- items: this block's own, then those of blocks that have not started
-        int block = blockIdx.x;
+        int block = blockIdx.x, beyond = 0x7fffffff;   // blocks from `beyond` on have no item
+        const uint64_t item_limit = 30 * limit;        // (these waits last as long as an item's loads)
         bool ok = true;
         for (int u = 0; ok; u++) {
             Item it;
-            it.kvh = -1;
-            if (block >= 0) it = find_item(a, p.nt, block);
+            it.kvh = block >= 0 ? -2 : -1;
+            if (block >= 0 && block < beyond) {
+                it = find_item(a, p.nt, block);
+                if (it.kvh == -2) beyond = block;
+            }
             if (block == 0) {   // report offsets that are cut
                 for (int b = lane; b < a.B; b += 32) {
                     const int64_t q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
@@ -377,7 +381,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 }
             }
             const int s = u % kItems;
-            ok = mbar_wait(b_ifree + 8 * s, ((u / kItems) & 1) ^ 1, abort, a.flags, limit);
+            ok = mbar_wait(b_ifree + 8 * s, ((u / kItems) & 1) ^ 1, abort, a.flags, item_limit);
             ok = __all_sync(FULL, ok);
             if (lane == 0 && ok) {
                 s_items[s] = it;
@@ -387,7 +391,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             if (block < 0 || !ok) break;
             // The next item is asked for when the last load of this one is issued: a whole item
             // ahead, the order of the items and not the CTAs' progress would decide who gets which.
-            if (!__all_sync(FULL, mbar_wait(b_next, u & 1, abort, a.flags, limit))) break;
+            if (!__all_sync(FULL, mbar_wait(b_next, u & 1, abort, a.flags, item_limit))) break;
             if (lane == 0) {
                 mbar_expect_tx(b_cancel, 16);
                 try_cancel(smem_addr(&s_cancel), b_cancel);
@@ -403,9 +407,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         }
       } else if (warp == 8) {
         // ---------------- loads
-        // One flat loop over all tiles of all items, here and in the products: the ring position
-        // then stays a loop counter that the compiler keeps in uniform registers, where the copies'
-        // and products' operands have to be (moving them there cost a fifth of the kernel's time).
+        // (one flat loop over the pairs of all items, here and in the products: the ring position is a
+        // plain loop counter)
         if (lane == 0) {
             Item w;
             int u = -1, j = 0, n = -1, nq = 0, kbeg = 0;
@@ -479,32 +482,25 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         auto wait = [&](uint32_t bar, uint32_t parity) {
             return mbar_poll(bar, parity) || mbar_wait(bar, parity, abort, a.flags, limit);
         };
-        auto commit = [&](uint32_t bar) {
-            mma_commit(bar);
-        };
         // S = Q_i K^T of stage s, once the rows of the scores before have been taken out of S
         auto scores = [&](int i, uint32_t s) -> bool {
             if (nscore > 0 && !wait(b_sfree, (nscore - 1) & 1)) return false;
             nscore++;
             tc_fence_after();
             const uint64_t da = dq + i * kStep, db = dk + s * (2 * kStep);
-            {
 #pragma unroll
-                for (int k = 0; k < D / 16; k++)
-                    mma_ss(tm, da + (k / 4) * 1024 + 2 * (k % 4), db + (k / 4) * 1024 + 2 * (k % 4), id_s, k != 0);
-                mma_commit(b_s + 8 * i);
-            }
+            for (int k = 0; k < D / 16; k++)
+                mma_ss(tm, da + (k / 4) * 1024 + 2 * (k % 4), db + (k / 4) * 1024 + 2 * (k % 4), id_s, k != 0);
+            mma_commit(b_s + 8 * i);
             return true;
         };
         // O_i += P_i V of stage s
         auto values = [&](int i, uint32_t s, bool first) {
             const uint64_t db = dv + s * (2 * kStep);
-            {
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; k++)
-                    mma_ts(tm + kO + D * i, tm + kP + 64 * i + 8 * k, db + 128 * k, id_o, k > 0 || !first);
-                mma_commit(b_pv + 8 * i);
-            }
+            for (int k = 0; k < kKeys / 16; k++)
+                mma_ts(tm + kO + D * i, tm + kP + 64 * i + 8 * k, db + 128 * k, id_o, k > 0 || !first);
+            mma_commit(b_pv + 8 * i);
         };
         // Pair `it` of the ring holds K_j and V_j-1.  A step issues S = Q K_j and then O += P V_j-1
         // for A and for B, so that scores are computed while the rows of the tile before are in the
@@ -556,12 +552,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 phA++;
                 if (ni == 2) phB++;
             }
-            commit(b_empty + 8 * s);
-            if (j + 1 == n) commit(b_qfree);   // the last scores are issued
+            mma_commit(b_empty + 8 * s);
+            if (j + 1 == n) mma_commit(b_qfree);   // the last scores are issued
             ready = j < n && wait(b_full + 8 * ((it + 1) % S), ((it + 1) / S) & 1);
             if (j < n && !ready) break;
         }
-        commit(b_drain);   // every issued MMA has finished before tensor memory is released
+        mma_commit(b_drain);   // every issued MMA has finished before tensor memory is released
         const uint64_t c0 = global_ns();
         while (!mbar_test(b_drain, 0) && global_ns() - c0 < limit) {
         }
