@@ -27,9 +27,9 @@
 // result is the same every time.  Short bounds (a window) take one CTA per
 // segment and no second kernel.
 //
-// Within a CTA eight rings of tiles of 64 tokens are filled by a warp each with
-// bulk copies, one tile ahead (one issuing thread per SM would not reach the
-// memory's rate).
+// Within a CTA each warp streams its own tiles of 64 tokens with bulk copies of
+// whole pages, one tile ahead (one issuing thread per SM would not reach the
+// memory's rate), and the warps' results are joined at a segment's end.
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -115,15 +115,16 @@ struct Span {
 // How many CTAs share a line of `total` weight: each has 8 tiles at least
 __device__ __forceinline__ int sharers(int64_t total) { return (int)min((int64_t)kCtas, (total + 7) / 8); }
 
-// PW warps share a tile (each takes 64 / PW of its tokens): two where the
-// accumulators of 8 heads leave registers for 16 warps, else one.
+// One warp per ring.  (Two warps to a tile, 16 in all with 128 registers each,
+// took 108 us where one took 96: what a tile costs beside its tokens was paid
+// twice.)  16 heads leave room for 8 warps' accumulators.
 template <int D, int NT>
 struct CachedSmem {
-    static constexpr int kRings = NT == 1 ? 10 : 8, PW = 1, kWarps = kRings * PW, kHalf = (kWarps + 1) / 2;
+    static constexpr int kWarps = NT == 1 ? 10 : 8, kHalf = (kWarps + 1) / 2;
     static constexpr int kTileBytes = kTile * KvPage<D>::kRowBytes;
-    static constexpr int kBars = kRings * kStages * kTileBytes;
-    static constexpr int kOk = kBars + kRings * kStages * 8;               // pages of each ring's tiles that hold tokens
-    static constexpr int kMax = kOk + (kRings * kStages * 4 + 15) / 16 * 16;                // [kWarps][16] maxima
+    static constexpr int kBars = kWarps * kStages * kTileBytes;
+    static constexpr int kOk = kBars + kWarps * kStages * 8;               // pages of each ring's tiles that hold tokens
+    static constexpr int kMax = kOk + (kWarps * kStages * 4 + 15) / 16 * 16;                // [kWarps][16] maxima
     static constexpr int kSum = kMax + kWarps * 16 * 4;                    // [kHalf][16] sums
     static constexpr int kAcc = kSum + (kHalf * 16 * 4 + 15) / 16 * 16;    // [kHalf][NT][D / 16][32 lanes] float4
     static constexpr int kTotal = kAcc + kHalf * NT * (D / 16) * 512;
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
 {
     using P = KvPage<D>;
     using L = CachedSmem<D, NT>;
-    constexpr int kRings = L::kRings, PW = L::PW, kWarps = L::kWarps, KB = 4 / PW;   // blocks of 16 tokens of a warp in a tile
+    constexpr int kWarps = L::kWarps, KB = kTile / 16;   // blocks of 16 tokens in a tile
     constexpr int G = D / 32, MT = D / 16;     // groups of 32 channels, 16-channel tiles of V^T
     constexpr bool kSplitP = sizeof(T) == 2 && !__is_same(T, __nv_bfloat16);
     extern __shared__ __align__(128) uint8_t smem[];
@@ -146,15 +147,9 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     constexpr int n = N, ppt = kTile / N;             // tokens of a page, pages of a tile
     constexpr int page_bytes = P::bytes(N);
-    const int ring = warp / PW, sub = warp % PW;      // this warp's ring and its part of a tile
-    const bool loader = sub == 0;                     // the warp that copies the ring's tiles
-    const uint32_t bar0 = smem_addr(smem + L::kBars) + ring * kStages * 8;
-    volatile uint32_t *okmask = (volatile uint32_t *)(smem + L::kOk) + ring * kStages;
-    auto ring_sync = [&]() {   // the warps of a ring (the barriers' ids are 1 .. 8)
-        if (PW > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + ring), "r"(32 * PW) : "memory");
-        else __syncwarp();
-    };
-    if (loader && lane == 0) {
+    const uint32_t bar0 = smem_addr(smem + L::kBars) + warp * kStages * 8;
+    volatile uint32_t *okmask = (volatile uint32_t *)(smem + L::kOk) + warp * kStages;
+    if (lane == 0) {
         for (int s = 0; s < kStages; s++) mbar_init(bar0 + 8 * s, 1);
         fence_barrier_init();
     }
@@ -227,7 +222,7 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
     auto enter = [&](Walk &w) {
         w.first = (int)max(R0 - w.W - kSegCost, (int64_t)0);
         w.last = (int)min(max(R1 - w.W - kSegCost, (int64_t)0), (int64_t)w.s.n);
-        w.tile = w.first + ring;
+        w.tile = w.first + warp;
         w.end = w.last;
     };
     auto next_segment = [&](Walk &w) -> bool {
@@ -267,7 +262,7 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
             const bool good = wanted && page >= 0 && page < a.num_pages;
             if (wanted && !good) set_flag(a.flags, MAPLE_DEVFLAG_BAD_INDEX);
             const uint32_t m = __ballot_sync(FULL, good);
-            if (lane == 0) okmask[s] = m;
+            if (lane == 0) okmask[s] = m;   // (read after the wait on the barrier and a warp barrier)
             const uint32_t bar = bar0 + 8 * s;
             if (lane == 0) {
                 if (m) mbar_expect_tx(bar, __popc(m) * page_bytes);
@@ -275,21 +270,18 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
             }
             __syncwarp();
             if (good)
-                bulk_g2s(smem_addr(smem + (ring * kStages + s) * L::kTileBytes + lane * page_bytes),
+                bulk_g2s(smem_addr(smem + (warp * kStages + s) * L::kTileBytes + lane * page_bytes),
                          a.pages + ((int64_t)page * a.kv_heads + pf.col / p.HB) * page_bytes, page_bytes, bar);
-            pf.tile += kRings;
+            pf.tile += kWarps;
             settle();
         }
     };
     uint32_t issued = 0, used = 0;   // tiles of this ring
-    if (loader) {
-        settle();
-        for (int s = 0; s < kStages; s++) {
-            if (have) issued++;
-            issue(s);
-        }
+    settle();
+    for (int s = 0; s < kStages; s++) {
+        if (have) issued++;
+        issue(s);
     }
-    ring_sync();   // (the masks of the first tiles)
 
     const int heads_per = a.heads / a.kv_heads;
     bool dead = false;
@@ -377,11 +369,11 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
             }
 
             // ---- this ring's tiles of the segment
-            for (int tile = cur.first + ring; tile < cur.last; tile += kRings) {
+            for (int tile = cur.first + warp; tile < cur.last; tile += kWarps) {
                 const int s = used % kStages;
                 if (!dead && !mbar_wait(bar0 + 8 * s, (used / kStages) & 1, abort, a.flags, kDefaultWaitNs)) dead = true;
                 dead = __any_sync(FULL, dead);
-                const uint8_t *buf = smem + (ring * kStages + s) * L::kTileBytes;
+                const uint8_t *buf = smem + (warp * kStages + s) * L::kTileBytes;
                 const uint32_t ok = okmask[s];
                 const int j0 = (cur.s.c0 + tile) * kTile;
                 const bool edge = j0 < cur.s.start || j0 + kTile > cur.s.len || ok != (1u << ppt) - 1;
@@ -389,7 +381,7 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
                     float S[NT][KB][4];
 #pragma unroll
                     for (int kb = 0; kb < KB; kb++) {
-                        const int k0 = (sub * KB + kb) * 16, pg = k0 / n, r0 = k0 % n;
+                        const int k0 = kb * 16, pg = k0 / n, r0 = k0 % n;
                         const uint8_t *base = buf + pg * page_bytes;
                         uint32_t w0[G], w1[G], pr0[G], pr1[G];
                         if (G == 4) {
@@ -485,7 +477,7 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
                     // ---- O^T += V^T P^T
 #pragma unroll
                     for (int kb = 0; kb < KB; kb++) {
-                        const int k0 = (sub * KB + kb) * 16, pg = k0 / n, r0 = k0 % n;
+                        const int k0 = kb * 16, pg = k0 / n, r0 = k0 % n;
                         const uint8_t *base = buf + pg * page_bytes;
                         const uint8_t *vb = base + n * (D / 2) + (r0 >> 4) * (8 * D) + lane * 16;
                         const int gg = g * (D / 8) / 32;   // the group of this lane's channels
@@ -553,12 +545,10 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
                             }
                     }
                 }
-                ring_sync();      // all of the ring's warps have read the tile
+                __syncwarp();     // the tile is read
                 used++;
-                if (loader) {
-                    if (have) issued++;
-                    issue(s);
-                }
+                if (have) issued++;
+                issue(s);
             }
 
             // ---- join the warps: common maximum, then sums in a fixed tree
@@ -598,7 +588,8 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
                     O[j][i][3] *= f[1];
                 }
             }
-            const int busy = min(kRings, ntile) * PW;    // (warps beyond the tiles hold zeros)
+            const int busy = min(kWarps, ntile);    // (warps beyond the tiles hold zeros)
+            if (busy <= 1) __syncthreads();         // the maxima are read before the next segment's are written
             for (int m = busy; m > 1;) {
                 const int half = (m + 1) / 2;
                 if (warp >= half && warp < m) {
@@ -675,7 +666,7 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
         }
         more = next_segment(cur);
     }
-    for (; loader && used < issued; used++)   // copies still in flight (only after a failed wait)
+    for (; used < issued; used++)   // copies still in flight (only after a failed wait)
         mbar_wait(bar0 + 8 * (used % kStages), (used / kStages) & 1, abort, a.flags, kDefaultWaitNs);
     asm volatile("griddepcontrol.launch_dependents;");
 }

@@ -395,6 +395,19 @@ def test_cached(lens, window, H, Hkv, d, n, dt):
     assert f.item() == 0
 
 
+def test_cached_many_short_and_some_long_sequences():
+    """Shares of the line that hold many short segments, empty ones and cuts of long ones; the same bits every time."""
+    lens = [[1, 70, 0, 200, 1, 3000, 64, 65][i % 8] + i % 3 for i in range(200)] + [15000, 1, 1, 1]
+    r = gen(41)
+    d, n = 64, 16
+    pages, table, kv = make_cache(r, lens, 2, d, n)
+    q, ln = r(len(lens), 8, d).to(BF16), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out = tw.cached_attention(q, pages, table, ln)
+    check_cached(out, q, kv, lens, d ** -0.5, 0, BF16)
+    for _ in range(20):
+        assert torch.equal(tw.cached_attention(q, pages, table, ln), out)
+
+
 @pytest.mark.parametrize("G", [1, 3, 8, 9, 17, 40])
 def test_cached_group_sizes(G):
     r = gen(G)
