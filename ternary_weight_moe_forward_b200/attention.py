@@ -148,7 +148,8 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias
     """y = (q_x weight^T) * (s_x alpha) (+ bias) (+ resid), q_x and s_x the int8 absmax codes and scales of x's rows.
 
     x bf16 [T][K] (rows may be strided), or the fp32 residual stream with `normalise` (its RMS-normed rows, rounded to
-    bf16, are quantised).  weight int8 [N][K], alpha fp32 [N], bias fp32 [N], resid fp32 [T][N] (may be `out`).
+    bf16, are quantised).  weight int8 [N][K], alpha fp32 [N], bias fp32 [N], resid fp32 [T][N] (may be `out`).  x must
+    not overlap `out`.
     """
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("x must be [T][K] and weight [N][K]")
@@ -170,6 +171,8 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias
         out = x.new_empty((T, N), dtype=out_dtype)
     elif out.shape != (T, N) or not out.is_contiguous():
         raise ValueError("out must be contiguous [T][N]")
+    elif T and out.data_ptr() == x.data_ptr():
+        raise ValueError("x must not be out")
     ydt = _OUT_TYPES.get(out.dtype)
     if ydt is None:
         raise ValueError("the output must be bf16 or fp32")

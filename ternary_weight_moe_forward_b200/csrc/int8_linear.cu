@@ -6,8 +6,9 @@
 // and every path gives the same bits.  Two paths, by the number of tokens:
 //   T <= 16   linear_rows_kernel: the weights are streamed once through
 //             warp-level int8 matrix instructions by all SMs, the tokens are
-//             quantised in the same kernel;
-//   T > 16    quantise_rows_kernel, then linear_gemm_kernel on tcgen05
+//             quantised (normed first, for at most 16384 values) in the same
+//             kernel;
+//   others    quantise_rows_kernel or the layer stack's norm kernel, then linear_gemm_kernel on tcgen05
 //             (kind::i8).  Up to 128 tokens the weights are the 128-row
 //             operand and all tokens one N tile (the weights are read once);
 //             above, the tokens are.
@@ -155,11 +156,45 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NT: column tiles of 8 tokens
-template <int NT>
-__global__ void __launch_bounds__(kRowWarps * 32, 2)
-linear_rows_kernel(const uint16_t *x, int64_t x_stride, int T, int K, const int8_t *w, LinearOut o)
+// Codes of bf16(RMSNorm(r)) of one fp32 row, one warp: the steps of
+// rmsnorm_token_warp (the same order of the sum, the same roundings) with the
+// normed row computed again for its maximum and for its codes instead of kept.
+__device__ __forceinline__ void norm_codes_warp(const float *r, int K, uint8_t *row, float *scale)
 {
+    const int lane = threadIdx.x & 31;
+    float acc = 0.0f;
+    for (int i = 0; i < K / 256; i++) {
+        const float4 v0 = *reinterpret_cast<const float4 *>(r + 256 * i + 8 * lane);
+        const float4 v1 = *reinterpret_cast<const float4 *>(r + 256 * i + 8 * lane + 4);
+        const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+        for (int m = 0; m < 8; m++) acc = __fmaf_rn(v[m], v[m], acc);
+    }
+    const float rms = __fsqrt_rn(__fadd_rn(__fdiv_rn(warp_tree_sum(acc), (float)K), 1e-6f));
+    auto normed = [&](int i) -> uint4 {
+        const float4 v0 = *reinterpret_cast<const float4 *>(r + 256 * i + 8 * lane);
+        const float4 v1 = *reinterpret_cast<const float4 *>(r + 256 * i + 8 * lane + 4);
+        const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        uint32_t pk[4];
+#pragma unroll
+        for (int m = 0; m < 4; m++)
+            pk[m] = (uint32_t)f32_to_bf16_bits(__fdiv_rn(v[2 * m], rms)) | ((uint32_t)f32_to_bf16_bits(__fdiv_rn(v[2 * m + 1], rms)) << 16);
+        return make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    };
+    float amax = 0.0f;
+    for (int i = 0; i < K / 256; i++) amax = absmax8(normed(i), amax);
+    amax = warp_max(amax);
+    const float inv = amax > 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;
+    for (int i = 0; i < K / 256; i++) reinterpret_cast<uint2 *>(row)[32 * i + lane] = quant8(normed(i), inv);
+    if (lane == 0) *scale = amax > 0.0f ? __fdiv_rn(amax, 127.0f) : 0.0f;
+}
+
+// NT: column tiles of 8 tokens; NORM: x is the fp32 residual stream
+template <int NT, bool NORM>
+__global__ void __launch_bounds__(kRowWarps * 32, 2)
+linear_rows_kernel(const void *xv, int64_t x_stride, int T, int K, const int8_t *w, LinearOut o)
+{
+    const uint16_t *x = (const uint16_t *)xv;
     extern __shared__ __align__(16) uint8_t codes[];        // [8 NT][pitch], then [2][16 warps][NT][32 lanes] int4
     __shared__ float s_scale[8 * NT], s_part[kRowWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -181,7 +216,12 @@ linear_rows_kernel(const uint16_t *x, int64_t x_stride, int T, int K, const int8
     if ((int64_t)blockIdx.x < tiles) fetch(blockIdx.x, warp);   // in flight while the tokens are quantised
 
     // ---- the tokens' codes, two per round (eight warps each); rows beyond T are 0
-    for (int r0 = 0; r0 < 8 * NT; r0 += 2) {
+    if (NORM && warp < 8 * NT) {   // a warp per token (16 warps, at most 16 tokens)
+        uint8_t *row = codes + warp * pitch;
+        if (warp < T) norm_codes_warp((const float *)xv + warp * x_stride, K, row, s_scale + warp);
+        for (int c = (warp < T ? K : 0) / 16 + lane; c < pitch / 16; c += 32) reinterpret_cast<uint4 *>(row)[c] = make_uint4(0, 0, 0, 0);
+    }
+    for (int r0 = 0; !NORM && r0 < 8 * NT; r0 += 2) {
         const int r = r0 + (warp >> 3), tid = threadIdx.x & 255;
         uint8_t *row = codes + r * pitch;
         if (r0 >= T) {   // (T is the same for all threads)
@@ -612,19 +652,27 @@ int rows_smem(int64_t T, int K)
     const int NT = T <= 8 ? 1 : 2;
     return 8 * NT * row_pitch(K) + 2 * kRowWarps * NT * 512;
 }
-bool rows_path(int64_t T, int K, bool normalise) { return T <= kRowTokens && !normalise && rows_smem(T, K) <= kRowCodes; }
+// With the norm every block reads the fp32 rows three times, which pays up to 16384
+// values: the two launches of the other path take 13.2 us for one row of 2048 into
+// 2560 columns and this kernel 9.2, 14.0 and 12.3 for 8 rows of 2048, 21.8 and 17.5
+// for 4 of 4096; but 14.4 and 21.4 for 16 of 2048, 37.1 and 39.0 for 4 of 8192 (16 of
+// 1024 are the one measured loss inside the rule: 10.6 and 12.2).
+bool rows_path(int64_t T, int K, bool normalise)
+{
+    return T <= kRowTokens && rows_smem(T, K) <= kRowCodes && (!normalise || T * K <= 16384);
+}
 
-template <int NT>
+template <int NT, bool NORM>
 int launch_rows(const maple_attn_linear_args &a, const LinearOut &o, cudaStream_t st)
 {
     const int smem = rows_smem(a.T, (int)a.K);
-    if (smem > 49152 && cudaFuncSetAttribute(linear_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowCodes) != cudaSuccess) {
+    if (smem > 49152 && cudaFuncSetAttribute(linear_rows_kernel<NT, NORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowCodes) != cudaSuccess) {
         cudaGetLastError();
         return MAPLE_ERR_CUDA;
     }
     const int64_t tiles = (a.N + 15) / 16;
-    linear_rows_kernel<NT><<<(unsigned)(tiles < 2 * 148 ? tiles : 2 * 148), kRowWarps * 32, smem, st>>>(
-        (const uint16_t *)a.x, a.x_stride, (int)a.T, (int)a.K, a.w, o);
+    linear_rows_kernel<NT, NORM><<<(unsigned)(tiles < 2 * 148 ? tiles : 2 * 148), kRowWarps * 32, smem, st>>>(
+        a.x, a.x_stride, (int)a.T, (int)a.K, a.w, o);
     return cudaGetLastError() == cudaSuccess ? MAPLE_OK : MAPLE_ERR_CUDA;
 }
 
@@ -687,7 +735,10 @@ extern "C" int maple_attn_linear(const maple_attn_linear_args *args, maple_strea
     cudaStream_t st = (cudaStream_t)stream;
     const int K = (int)a.K;
     const LinearOut o{a.alpha, a.bias, a.resid, a.y, a.N, a.y_dtype == MAPLE_BF16};
-    if (rows_path(a.T, K, a.normalise)) return a.T <= 8 ? launch_rows<1>(a, o, st) : launch_rows<2>(a, o, st);
+    if (rows_path(a.T, K, a.normalise != 0)) {
+        if (a.normalise) return a.T <= 8 ? launch_rows<1, true>(a, o, st) : launch_rows<2, true>(a, o, st);
+        return a.T <= 8 ? launch_rows<1, false>(a, o, st) : launch_rows<2, false>(a, o, st);
+    }
 
     int8_t *q = (int8_t *)a.workspace;
     float *s = (float *)((char *)a.workspace + round256(a.T * a.K));

@@ -74,7 +74,7 @@ def test_linear_extreme_codes_strided_rows_and_in_place():
     assert tw.int8_linear(x[:0], w, al).shape == (0, 64)
 
 
-@pytest.mark.parametrize("T,K", [(1, 2048), (9, 256), (100, 2048), (3, 8192), (2, 32768)])
+@pytest.mark.parametrize("T,K", [(1, 2048), (9, 256), (100, 2048), (3, 8192), (2, 32768), (16, 2048), (17, 2048)])
 def test_linear_normalise(T, K):
     """The normed form quantises bf16(x / rms): off by one rounding of the norm at most, so one code in a while."""
     r = gen(T + K)
@@ -88,6 +88,29 @@ def test_linear_normalise(T, K):
     most = 2.0 * 127 * max(1.0, K * 2.0 ** -12) * al * (amax / 127)
     assert ((got - want).abs() <= most).all()
     assert (got == want).float().mean() > 0.5 or K > 8192
+
+
+def test_linear_normalise_is_the_same_for_few_and_many_tokens():
+    """The norm inside the kernel for few tokens and the one of its own for many give the same codes, so the same bits."""
+    r = gen(77)
+    x, w, al = 3 * r(40, 2048), torch.clamp(torch.round(r(200, 2048) * 40), -127, 127).to(torch.int8), r(200)
+    x[5] = 0
+    many = tw.int8_linear(x, w, al, normalise=True)
+    for a, b in ((0, 1), (3, 11), (0, 16), (24, 40)):
+        assert torch.equal(tw.int8_linear(x[a:b], w, al, normalise=True), many[a:b])
+    x, w = x[:, :1024].contiguous(), w[:, :1024].contiguous()       # narrow enough for 16 rows in one kernel
+    many = tw.int8_linear(x, w, al, normalise=True)
+    for a, b in ((0, 1), (3, 11), (0, 16), (24, 40)):
+        assert torch.equal(tw.int8_linear(x[a:b], w, al, normalise=True), many[a:b])
+
+
+def test_linear_refuses_to_write_over_its_input():
+    x = torch.ones(2, 256, device="cuda")
+    w, al = torch.ones(256, 256, dtype=torch.int8, device="cuda"), torch.ones(256, device="cuda")
+    with pytest.raises(ValueError, match="x must not be out"):
+        tw.int8_linear(x, w, al, normalise=True, out=x)
+    y = tw.int8_linear(x, w, al, resid=x, normalise=True)           # x may be read twice
+    torch.testing.assert_close(y, x + tw.int8_linear(x, w, al, normalise=True), rtol=2.0 ** -23, atol=0)
 
 
 # ---------------------------------------------------------------- norm, rotation, cache
