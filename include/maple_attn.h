@@ -151,7 +151,8 @@ int maple_attn_kv_read(const maple_attn_read_args *args, maple_stream_t stream);
  * j <= position).  A query that sees no key gives a row of zeros and lse -inf.
  * out[t][h] = sum_j softmax_j(scale * q.k_j) v_j; lse (may be NULL) fp32
  * [Tq][heads] = log sum_j exp(scale * q.k_j).  Rows of out and lse that belong
- * to no sequence are left as they were.  What stands in masked keys and values
+ * to no sequence are left as they were; out and lse overlap nothing that the
+ * call reads.  What stands in masked keys and values
  * (infinities, NaN) does not reach the output.
  * max_q bounds every lq from above (a sequence with more query rows raises
  * MAPLE_FLAG_BAD_INDEX and loses the rows beyond max_q); offsets that fall or

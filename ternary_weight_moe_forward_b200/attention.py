@@ -251,7 +251,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     q [Tq][heads][d], k and v [Tk][kv_heads][d], bf16 or fp16; cu_q, cu_k int32 [B+1], the rows where sequences begin;
     max_q at least the longest sequence's query rows.  A sequence's queries are its last positions.  scale defaults to
     d^-1/2; window > 0 lets a query see that many positions, its own included.  Rows outside every sequence are not
-    written (`out` keeps them).
+    written (`out` keeps them); `out` must not overlap q, k or v.
     """
     dt = q.dtype
     if dt not in _HEAD_TYPES:
@@ -269,6 +269,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
         out = torch.empty_like(q, memory_format=_CONTIGUOUS)
     elif out.dtype is not dt or out.shape != (Tq, H, d) or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's type and shape")
+    elif Tq and out.data_ptr() in (q.data_ptr(), k.data_ptr(), v.data_ptr()):
+        raise ValueError("out must not be q, k or v")
     lse = q.new_empty((Tq, H), dtype=torch.float32) if return_lse else None
     _call("prompt", _PROMPT.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),

@@ -674,13 +674,14 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
 // Joins the partial results of segments that several CTAs share: one CTA per
 // (sequence, column, head), its 8 warps taking every eighth partial result and
 // summed in order, so that all loads are in flight at once (a loop over the
-// partial results by one thread per output cost 40 us for 75 of them).
+// partial results by one thread per output cost 40 us for 75 of them).  A warp's
+// first ten partial results are loaded before their factors are known: one
+// sequence of 131071 tokens takes 22.6 us in all instead of 26.5.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(256) combine_kernel(const CachedK p)
+__global__ void __launch_bounds__(256, 4) combine_kernel(const CachedK p)
 {
-    constexpr int V = D / 32;      // channels of a lane
+    constexpr int V = D / 32, kEarly = 10;      // channels of a lane, partial results loaded before their factors are known
     __shared__ float s_f[kCtas], s_l[8], s_acc[8][D], s_m[8];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const maple_attn_cached_args &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.x / p.cols, col = blockIdx.x - b * p.cols, h = blockIdx.y;
@@ -690,6 +691,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CachedK p)
     s.load(a, b);
     e.load(a, a.B - 1);
     if (s.n == 0) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // (the lengths are not cached_kernel's)
     const int64_t total = p.prefix[a.B - 1] + (int64_t)p.cols * (e.n + kSegCost);
     const int ns = sharers(total);
     const int64_t W = p.prefix[b] + (int64_t)col * (s.n + kSegCost);
@@ -699,8 +701,18 @@ __global__ void __launch_bounds__(256) combine_kernel(const CachedK p)
     if (i0 == i1) return;
     const int first_slot = 2 * i0 + (total * i0 / ns >= W ? 0 : 1);   // (later shares begin inside the segment)
     auto at = [&](int i) { return (int64_t)(i == i0 ? first_slot : 2 * i) * 8 * NT + h; };
-    // factors of the partial results
     const int np = i1 - i0 + 1;
+    // the first partial results of the warp, on their way under the factors
+    auto fetch = [&](int i, float (&x)[V]) {
+        const float *src = p.part_o + at(i0 + i) * D + V * lane;
+        if (V == 4) *(float4 *)x = *reinterpret_cast<const float4 *>(src);
+        else *(float2 *)x = *reinterpret_cast<const float2 *>(src);
+    };
+    float early[kEarly][V];
+#pragma unroll
+    for (int j = 0; j < kEarly; j++)
+        if (warp + 8 * j < np) fetch(warp + 8 * j, early[j]);
+    // factors of the partial results
     float2 ml = make_float2(-INFINITY, 0.0f);
     if ((int)threadIdx.x < np) ml = *reinterpret_cast<const float2 *>(p.part_ml + at(i0 + threadIdx.x) * 2);
     const float wm = warp_max(ml.x);
@@ -717,13 +729,18 @@ __global__ void __launch_bounds__(256) combine_kernel(const CachedK p)
     float acc[V];
 #pragma unroll
     for (int v = 0; v < V; v++) acc[v] = 0.0f;
-#pragma unroll 4
-    for (int i = warp; i < np; i += 8) {
-        const float *src = p.part_o + at(i0 + i) * D + V * lane;
+#pragma unroll
+    for (int j = 0; j < kEarly; j++)
+        if (warp + 8 * j < np) {
+            const float fi = s_f[warp + 8 * j];
+#pragma unroll
+            for (int v = 0; v < V; v++) acc[v] = fmaf(early[j][v], fi, acc[v]);
+        }
+#pragma unroll 5
+    for (int i = warp + 8 * kEarly; i < np; i += 8) {
         const float fi = s_f[i];
         float x[V];
-        if (V == 4) *(float4 *)x = *reinterpret_cast<const float4 *>(src);
-        else *(float2 *)x = *reinterpret_cast<const float2 *>(src);
+        fetch(i, x);
 #pragma unroll
         for (int v = 0; v < V; v++) acc[v] = fmaf(x[v], fi, acc[v]);
     }

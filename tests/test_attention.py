@@ -104,6 +104,13 @@ def test_linear_normalise_is_the_same_for_few_and_many_tokens():
         assert torch.equal(tw.int8_linear(x[a:b], w, al, normalise=True), many[a:b])
 
 
+def test_prompt_refuses_to_write_over_its_input():
+    q, k, v = (torch.ones(4, 2, 64, dtype=torch.float16, device="cuda") for _ in range(3))
+    for x in (q, k, v):
+        with pytest.raises(ValueError, match="out must not be"):
+            tw.prompt_attention(q, k, v, cu([4]), cu([4]), 4, out=x)
+
+
 def test_linear_refuses_to_write_over_its_input():
     x = torch.ones(2, 256, device="cuda")
     w, al = torch.ones(256, 256, dtype=torch.int8, device="cuda"), torch.ones(256, device="cuda")
