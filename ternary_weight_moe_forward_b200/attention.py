@@ -136,7 +136,7 @@ def _pages(pages, head_dim: int):
     if pages.dtype is not torch.uint8 or pages.dim() != 3 or not pages.is_contiguous():
         raise ValueError("pages must be a contiguous uint8 [num_pages][kv_heads][page bytes]")
     P, Hkv, size = pages.shape
-    n = 4 * size // (5 * head_dim)
+    n = 4 * size // (5 * head_dim) if head_dim else 0
     if 4 * size != 5 * head_dim * n or n not in _PAGE_SIZES:
         raise ValueError("the pages do not fit this head_dim")
     return P, Hkv, n

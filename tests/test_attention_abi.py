@@ -123,3 +123,9 @@ def test_python_refuses_wrong_tensors():
                             torch.zeros(2, dtype=torch.int32))
     with pytest.raises(tw.MapleError):
         tw.kv_pages(1, 1, 96)
+
+
+@pytest.mark.parametrize("head_dim", [0, -128, 32, 96, 256])
+def test_python_refuses_a_head_dim_that_the_pages_do_not_have(head_dim):
+    with pytest.raises(ValueError):
+        tw.kv_read(torch.zeros(1, 2, 2560, dtype=torch.uint8), torch.zeros(2, dtype=torch.int64), head_dim)
