@@ -477,7 +477,7 @@ linear_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_const
         asm volatile("griddepcontrol.wait;" ::: "memory");   // (the scales)
         const int q = warp & 3, half = (warp - 4) >> 2, r = 32 * q + lane;
         const LinearOut &o = p.o;
-        uint32_t n = 0;
+        uint32_t n = 0, piece = 0;      // tiles, pieces of 32 x 32 outputs that this warp has handed to TMA
         for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, n++) {
             const int64_t ta = tile / p.tiles_b, tb = tile - ta * p.tiles_b;
             const int64_t row = ta * 128 + r;
@@ -545,8 +545,11 @@ linear_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_const
                                 v[c + 3] = __fadd_rn(re.w, v[c + 3]);
                             }
                         }
-                        // (two pieces of bf16 fit the warp's 4 KB, one of fp32: the piece before has left it)
-                        uint8_t *st = s_out + (warp - 4) * 4096 + (o.y_bf16 ? ((c0 >> 6) & 1) * 2048 : 0);
+                        // Two pieces of bf16 fit the warp's 4 KB, one of fp32.  The halves alternate from piece to
+                        // piece over all tiles of the CTA: the wait below leaves the newest store pending, which
+                        // then always reads the other half.  (Counted from each tile's start, the last piece of a
+                        // tile with an odd number of them and the next tile's first would share one.)
+                        uint8_t *st = s_out + (warp - 4) * 4096 + (o.y_bf16 ? (piece++ & 1) * 2048 : 0);
                         if (lane == 0) {
                             if (o.y_bf16) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                             else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
