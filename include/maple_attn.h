@@ -76,6 +76,8 @@ int64_t maple_attn_page_bytes(int32_t head_dim, int32_t page_size);
  * normalise != 0: x is the fp32 residual stream and the row that is quantised
  * is bf16(RMSNorm(x)) (norm weights 1, eps 1e-6, the layer stack's rule; K must
  * be a multiple of 256 then).
+ * A row of x that holds a NaN or an infinity gives a row of NaN, with normalise
+ * also one whose sum of squares is beyond fp32 (values of 10^18 and more).
  * resid may be y; y overlaps nothing else that the call reads.
  * Limits: K a multiple of 16, 16 <= K <= 32768; 1 <= N; T*N and N*K < 2^40.
  * T == 0 is a no-op.

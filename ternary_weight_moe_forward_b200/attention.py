@@ -149,7 +149,7 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias
 
     x bf16 [T][K] (rows may be strided), or the fp32 residual stream with `normalise` (its RMS-normed rows, rounded to
     bf16, are quantised).  weight int8 [N][K], alpha fp32 [N], bias fp32 [N], resid fp32 [T][N] (may be `out`).  x must
-    not overlap `out`.
+    not overlap `out`.  A row of x with a NaN or an infinity gives a row of NaN.
     """
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("x must be [T][K] and weight [N][K]")

@@ -8,10 +8,11 @@
 //             warp-level int8 matrix instructions by all SMs, the tokens are
 //             quantised (normed first, for at most 16384 values) in the same
 //             kernel;
-//   others    quantise_rows_kernel or the layer stack's norm kernel, then linear_gemm_kernel on tcgen05
-//             (kind::i8).  Up to 128 tokens the weights are the 128-row
-//             operand and all tokens one N tile (the weights are read once);
-//             above, the tokens are.
+//   others    quantise_rows_kernel or norm_quantise_rows_kernel, then
+//             linear_gemm_kernel on tcgen05 (kind::i8).  Up to 128 tokens the
+//             weights are the 128-row operand and all tokens one N tile (the
+//             weights are read once); above, the tokens are.
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -26,6 +27,24 @@ using namespace maple;
 namespace {
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+// The largest absolute value of a row, or NaN if the row holds one: its codes mean
+// nothing then, and a scale of NaN makes the row's outputs NaN.  (An infinity does
+// the same without help: scale infinite, all codes 0.)
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float warp_max_nan(float v)
+{
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v = max_nan(v, __shfl_xor_sync(FULL, v, o));
+    return v;
+}
+__device__ __forceinline__ float row_inv(float amax) { return amax > 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f; }   // (a zero row: codes 0)
+__device__ __forceinline__ float row_scale(float amax) { return amax > 0.0f ? __fdiv_rn(amax, 127.0f) : amax; }
 
 // Int8 absmax codes of bf16 rows, one warp per row.  NV > 0: the row (at most
 // 256 NV values) stays in registers between the maximum and the codes, all of
@@ -47,7 +66,7 @@ __device__ __forceinline__ float absmax8(const uint4 &v, float amax)
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int m = 0; m < 4; m++)
-        amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(w[m] & 0xffffu)), fabsf(bf16_bits_to_f32(w[m] >> 16))));
+        amax = max_nan(amax, max_nan(fabsf(bf16_bits_to_f32(w[m] & 0xffffu)), fabsf(bf16_bits_to_f32(w[m] >> 16))));
     return amax;
 }
 
@@ -72,8 +91,8 @@ __global__ void __launch_bounds__(256) quantise_rows_kernel(const uint16_t *x, i
     } else {
         for (int c = lane; c < n; c += 32) amax = absmax8(__ldg(xr + c), amax);
     }
-    amax = warp_max(amax);
-    const float inv = amax > 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;   // (a zero row: codes 0)
+    amax = warp_max_nan(amax);
+    const float inv = row_inv(amax);
     if (NV > 0) {
 #pragma unroll
         for (int i = 0; i < NV; i++)
@@ -81,10 +100,27 @@ __global__ void __launch_bounds__(256) quantise_rows_kernel(const uint16_t *x, i
     } else {
         for (int c = lane; c < n; c += 32) qr[c] = quant8(__ldg(xr + c), inv);
     }
-    if (lane == 0) s[t] = amax > 0.0f ? __fdiv_rn(amax, 127.0f) : 0.0f;
+    if (lane == 0) s[t] = row_scale(amax);
 }
 
-// One warp per row: bf16(RMSNorm(row)) in shared memory, then its codes
+// Sum of the squares of a row, one warp, in the order of rmsnorm_token_warp
+__device__ __forceinline__ float sum_squares_warp(const float *r, int K)
+{
+    const int lane = threadIdx.x & 31;
+    float acc = 0.0f;
+    for (int i = 0; i < K / 256; i++) {
+        const float4 v0 = *reinterpret_cast<const float4 *>(r + 256 * i + 8 * lane);
+        const float4 v1 = *reinterpret_cast<const float4 *>(r + 256 * i + 8 * lane + 4);
+        const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+        for (int m = 0; m < 8; m++) acc = __fmaf_rn(v[m], v[m], acc);
+    }
+    return warp_tree_sum(acc);
+}
+
+// One warp per row: bf16(RMSNorm(row)) in shared memory, then its codes.  A row
+// whose sum of squares is not finite has no norm: its normed values come out as
+// zeros (so only rows of zeros are looked at again), its scale has to be NaN.
 __global__ void __launch_bounds__(128) norm_quantise_rows_kernel(const float *x, int64_t stride, int64_t T, int K,
                                                                  int8_t *q, float *s)
 {
@@ -99,10 +135,11 @@ __global__ void __launch_bounds__(128) norm_quantise_rows_kernel(const float *x,
     float amax = 0.0f;
     for (int c = lane; c < K / 2; c += 32) {
         const uint32_t w = reinterpret_cast<const uint32_t *>(row)[c];
-        amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(w & 0xffffu)), fabsf(bf16_bits_to_f32(w >> 16))));
+        amax = max_nan(amax, max_nan(fabsf(bf16_bits_to_f32(w & 0xffffu)), fabsf(bf16_bits_to_f32(w >> 16))));
     }
-    amax = warp_max(amax);
-    const float inv = amax > 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;
+    amax = warp_max_nan(amax);
+    const float inv = row_inv(amax);
+    if (!(amax > 0.0f) && !(sum_squares_warp(x + t * stride, K) < INFINITY)) amax = NAN;
     for (int c = lane; c < K / 4; c += 32) {
         const uint2 w = reinterpret_cast<const uint2 *>(row)[c];
         uint32_t pk = 0;
@@ -114,7 +151,7 @@ __global__ void __launch_bounds__(128) norm_quantise_rows_kernel(const float *x,
         }
         reinterpret_cast<uint32_t *>(q + t * K)[c] = pk;
     }
-    if (lane == 0) s[t] = amax > 0.0f ? __fdiv_rn(amax, 127.0f) : 0.0f;
+    if (lane == 0) s[t] = row_scale(amax);
 }
 
 struct LinearOut {
@@ -162,15 +199,7 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
 __device__ __forceinline__ void norm_codes_warp(const float *r, int K, uint8_t *row, float *scale)
 {
     const int lane = threadIdx.x & 31;
-    float acc = 0.0f;
-    for (int i = 0; i < K / 256; i++) {
-        const float4 v0 = *reinterpret_cast<const float4 *>(r + 256 * i + 8 * lane);
-        const float4 v1 = *reinterpret_cast<const float4 *>(r + 256 * i + 8 * lane + 4);
-        const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-        for (int m = 0; m < 8; m++) acc = __fmaf_rn(v[m], v[m], acc);
-    }
-    const float rms = __fsqrt_rn(__fadd_rn(__fdiv_rn(warp_tree_sum(acc), (float)K), 1e-6f));
+    const float rms = __fsqrt_rn(__fadd_rn(__fdiv_rn(sum_squares_warp(r, K), (float)K), 1e-6f));
     auto normed = [&](int i) -> uint4 {
         const float4 v0 = *reinterpret_cast<const float4 *>(r + 256 * i + 8 * lane);
         const float4 v1 = *reinterpret_cast<const float4 *>(r + 256 * i + 8 * lane + 4);
@@ -184,9 +213,9 @@ __device__ __forceinline__ void norm_codes_warp(const float *r, int K, uint8_t *
     float amax = 0.0f;
     for (int i = 0; i < K / 256; i++) amax = absmax8(normed(i), amax);
     amax = warp_max(amax);
-    const float inv = amax > 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;
+    const float inv = row_inv(amax);
     for (int i = 0; i < K / 256; i++) reinterpret_cast<uint2 *>(row)[32 * i + lane] = quant8(normed(i), inv);
-    if (lane == 0) *scale = amax > 0.0f ? __fdiv_rn(amax, 127.0f) : 0.0f;
+    if (lane == 0) *scale = rms < INFINITY ? row_scale(amax) : NAN;   // (a sum of squares that is not finite: no norm)
 }
 
 // NT: column tiles of 8 tokens; NORM: x is the fp32 residual stream
@@ -235,16 +264,16 @@ linear_rows_kernel(const void *xv, int64_t x_stride, int T, int K, const int8_t 
             const uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int m = 0; m < 4; m++)
-                amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(q[m] & 0xffffu)), fabsf(bf16_bits_to_f32(q[m] >> 16))));
+                amax = max_nan(amax, max_nan(fabsf(bf16_bits_to_f32(q[m] & 0xffffu)), fabsf(bf16_bits_to_f32(q[m] >> 16))));
         }
-        amax = warp_max(amax);
+        amax = warp_max_nan(amax);
         __syncthreads();
         if (lane == 0) s_part[warp] = amax;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; i++) amax = fmaxf(amax, s_part[(warp & 8) + i]);
+        for (int i = 0; i < 8; i++) amax = max_nan(amax, s_part[(warp & 8) + i]);
         if (r >= T) amax = 0.0f;
-        const float inv = amax > 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;
+        const float inv = row_inv(amax);
         for (int c = tid; c < pitch / 8; c += 256) {
             uint32_t pk[2] = {0u, 0u};
             if (c < K / 8 && amax > 0.0f) {
@@ -258,7 +287,7 @@ linear_rows_kernel(const void *xv, int64_t x_stride, int T, int K, const int8_t 
             }
             reinterpret_cast<uint2 *>(row)[c] = make_uint2(pk[0], pk[1]);
         }
-        if (tid == 0) s_scale[r] = amax > 0.0f ? __fdiv_rn(amax, 127.0f) : 0.0f;
+        if (tid == 0) s_scale[r] = row_scale(amax);
     }
     __syncthreads();
 

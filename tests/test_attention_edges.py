@@ -44,3 +44,55 @@ def test_linear_tiles_that_follow_one_another(T, N, K):
     want = linear_ref(x, w, al).to(BF16)
     for _ in range(20):
         assert torch.equal(tw.int8_linear(x, w, al, out_dtype=BF16), want)
+
+
+@pytest.mark.parametrize("T", [1, 3, 8, 9, 16, 17, 100, 130, 300])
+@pytest.mark.parametrize("K,N", [(256, 64), (2048, 40), (8192, 24)])
+@pytest.mark.parametrize("normalise", [False, True])
+def test_linear_rows_that_are_not_finite(T, K, N, normalise):
+    """A NaN or an infinity anywhere in a row makes that row's outputs NaN, and no other row's."""
+    r = gen(T + K + N)
+    x, w, al, bias = 3 * r(T, K), ints(r, N, K), r(N), r(N)
+    x = x if normalise else x.to(BF16)
+    resid = r(T, N)
+    want = tw.int8_linear(x, w, al, bias, resid, normalise=normalise)
+    assert want.isfinite().all()
+    for n, bad in enumerate((math.nan, -math.nan, math.inf, -math.inf)):
+        for at in (0, 31, 255, K - 1):
+            row = (3 * n + at) % T
+            y = x.clone()
+            y[row, at] = bad
+            got = tw.int8_linear(y, w, al, bias, resid, normalise=normalise)
+            assert got[row].isnan().all()
+            keep = torch.arange(T, device="cuda") != row
+            assert torch.equal(got[keep], want[keep])
+    y = x.clone()
+    y[:, 1], y[:, 2] = math.nan, math.inf
+    assert tw.int8_linear(y, w, al, normalise=normalise, out_dtype=BF16).isnan().all()
+
+
+@pytest.mark.parametrize("T", [2, 40])
+def test_linear_norm_beyond_fp32(T):
+    """A row whose squares do not fit fp32 has no norm; rows of zeros, and of values whose squares vanish, have one."""
+    r = gen(T)
+    x, w, al = r(T, 512), ints(r, 33, 512), r(33)
+    x[0] = 1e30
+    x[1] = 0
+    got = tw.int8_linear(x, w, al, normalise=True)
+    assert got[0].isnan().all() and (got[1] == 0).all() and got[2:].isfinite().all()
+    x[1] = 1e-30
+    assert (tw.int8_linear(x, w, al, normalise=True)[1].abs() <= 1e-20).all()
+
+
+def test_a_token_that_is_not_finite_stays_so_in_the_layer():
+    """A NaN in one token's residual: its own row, and the later rows of its sequence, are NaN; another sequence is not."""
+    from ternary_weight_moe_forward_b200 import synth
+    attn = tw.AttentionLayer(256, 4, 2, 64, synth.attention_weights(256, 4, 2, 64, 5), 4, page_size=16)
+    lens, s = [12, 9], torch.arange(21, device="cuda") + torch.cat([torch.zeros(12), torch.full((9,), 4.0)]).long().cuda()
+    pos = torch.cat([torch.arange(m, device="cuda") for m in lens])
+    c = torch.tensor([0, 12, 21], dtype=torch.int32, device="cuda")
+    base = gen(8)(21, 256)
+    want = attn.prompt(base.clone(), pos, s, c, 12)
+    base[5, 17] = math.nan
+    got = attn.prompt(base.clone(), pos, s, c, 12)
+    assert torch.equal(got[:5], want[:5]) and torch.equal(got[12:], want[12:]) and got[5:12].isnan().all()
