@@ -686,12 +686,13 @@ __global__ void __launch_bounds__(256, 4) combine_kernel(const CachedK p)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.x / p.cols, col = blockIdx.x - b * p.cols, h = blockIdx.y;
     const int heads_per = a.heads / a.kv_heads, kvh = col / p.HB, h0 = (col - kvh * p.HB) * 8 * NT;
-    if (h >= heads_per - h0) return;
     Span s, e;
     s.load(a, b);
     e.load(a, a.B - 1);
-    if (s.n == 0) return;
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // (the lengths are not cached_kernel's)
+    // Every block waits (the lengths are not cached_kernel's, they are read before): if all of them could return
+    // first, as for a batch without a token, what follows this kernel would not be ordered behind cached_kernel.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (s.n == 0 || h >= heads_per - h0) return;
     const int64_t total = p.prefix[a.B - 1] + (int64_t)p.cols * (e.n + kSegCost);
     const int ns = sharers(total);
     const int64_t W = p.prefix[b] + (int64_t)col * (s.n + kSegCost);

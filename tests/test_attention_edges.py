@@ -96,3 +96,18 @@ def test_a_token_that_is_not_finite_stays_so_in_the_layer():
     base[5, 17] = math.nan
     got = attn.prompt(base.clone(), pos, s, c, 12)
     assert torch.equal(got[:5], want[:5]) and torch.equal(got[12:], want[12:]) and got[5:12].isnan().all()
+
+
+@pytest.mark.parametrize("H,Hkv,d,n", [(16, 2, 128, 64), (5, 1, 64, 16)])
+def test_cached_batch_without_a_token(H, Hkv, d, n):
+    """No sequence has a token, on a block table wide enough for two kernels: zeros, and the next kernel sees them."""
+    pages = tw.kv_pages(4, Hkv, d, n)
+    pages.fill_(0xFF)
+    for B in (1, 3, 200, 2000):
+        table = torch.zeros(B, 4096, dtype=torch.int32, device="cuda")
+        q = gen(B)(B, H, d).to(BF16)
+        for lens in (torch.zeros(B, dtype=torch.int32, device="cuda"), torch.full((B,), -5, dtype=torch.int32, device="cuda")):
+            for _ in range(10):
+                junk = torch.full((B, H, d), 7.0, dtype=BF16, device="cuda")   # (its memory is the next output's)
+                del junk
+                assert torch.count_nonzero(tw.cached_attention(q, pages, table, lens) * 1.0).item() == 0
