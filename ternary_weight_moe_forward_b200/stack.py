@@ -102,6 +102,10 @@ class DecoderStack:
     def _run(self, resid: torch.Tensor, step) -> torch.Tensor:
         if resid.dtype is not torch.float32 or resid.dim() != 2 or not resid.is_contiguous():
             raise ValueError("resid must be contiguous fp32 [T][d_model]")
+        # (before anything is changed: a layer that refuses a call has a residual and a cache from the layers before it)
+        most = min((moe.max_tokens for _, moe in self.layers), default=resid.shape[0])
+        if resid.shape[0] > most:
+            raise ValueError(f"{resid.shape[0]} tokens, but a layer takes at most {most}")
         stream = torch.cuda.current_stream(resid.device).cuda_stream
         with torch.cuda.device(resid.device):
             for attn, moe in self.layers:
