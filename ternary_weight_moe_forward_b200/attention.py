@@ -131,14 +131,14 @@ def kv_pages(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, 
     return torch.zeros(num_pages, kv_heads, b, dtype=torch.uint8, device=device)
 
 
-def _pages(pages, head_dim: int):
+def _pages(pages, head_dim: int, page_size: int | None):
     """(num_pages, kv_heads, page_size) of a cache tensor."""
     if pages.dtype is not torch.uint8 or pages.dim() != 3 or not pages.is_contiguous():
         raise ValueError("pages must be a contiguous uint8 [num_pages][kv_heads][page bytes]")
     P, Hkv, size = pages.shape
     n = 4 * size // (5 * head_dim) if head_dim else 0
-    if 4 * size != 5 * head_dim * n or n not in _PAGE_SIZES:
-        raise ValueError("the pages do not fit this head_dim")
+    if 4 * size != 5 * head_dim * n or n not in _PAGE_SIZES or page_size not in (None, n):
+        raise ValueError("the pages do not fit this head_dim" + ("" if page_size is None else " and page_size"))
     return P, Hkv, n
 
 
@@ -188,12 +188,12 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
                  q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
                  interleaved: bool = False, v: torch.Tensor | None = None, pages: torch.Tensor | None = None,
-                 slots: torch.Tensor | None = None, flags: torch.Tensor | None = None):
+                 slots: torch.Tensor | None = None, flags: torch.Tensor | None = None, page_size: int | None = None):
     """(q', k'): every head normed (RMS, weights fp32 [head_dim] or 1) and rotated by its position.
 
     q [T][heads][d], k [T][kv_heads][d], bf16 or fp16 (views of one projection are taken as they are); positions int64
     [T]; inv_freq float64 [rotary_dim/2] in radians per position.  With `pages`, `v` and `slots` (int64 [T], < 0: do not
-    store, distinct otherwise) the rotated keys and the values are also written to the cache.
+    store, distinct otherwise) the rotated keys and the values are also written to the cache (page_size: see kv_read).
     """
     dt = q.dtype
     if dt not in _HEAD_TYPES:
@@ -202,18 +202,18 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_
     Tk, Hkv, dk, ks = _heads(k, dt, "k must be [T][kv_heads][d] of q's type, a token's heads contiguous")
     if Tk != T or dk != d:
         raise ValueError("k must hold the same tokens and head_dim as q")
-    dev = _device(q, k, positions, inv_freq, q_weight, k_weight, v, pages, slots, flags)
     vs = n = P = vp = pp = 0
     if pages is not None:
         if v is None or slots is None:
             raise ValueError("pages, v and slots go together")
         vs = _heads(v, dt, "v must be [T][kv_heads][d] of q's type, a token's heads contiguous")[3]
-        P, Hc, n = _pages(pages, d)
+        P, Hc, n = _pages(pages, d, page_size)
         if v.shape != k.shape or Hc != Hkv:
             raise ValueError("v must have the shape of k, and the cache its heads")
         vp, pp = v.data_ptr(), pages.data_ptr()
     elif v is not None or slots is not None:
         raise ValueError("pages, v and slots go together")
+    dev = _device(q, k, positions, inv_freq, q_weight, k_weight, v, pages, slots, flags)
     qo = torch.empty_like(q, memory_format=_CONTIGUOUS)
     ko = torch.empty_like(k, memory_format=_CONTIGUOUS)
     rot = inv_freq.shape[0]
@@ -229,11 +229,16 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_
 
 
 def kv_read(pages: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: torch.dtype = torch.bfloat16,
-            flags: torch.Tensor | None = None):
-    """(k, v) [n][kv_heads][head_dim]: the values that the cache holds at `slots` (int64 [n]; < 0 reads as zeros)."""
+            flags: torch.Tensor | None = None, page_size: int | None = None):
+    """(k, v) [n][kv_heads][head_dim]: the values that the cache holds at `slots` (int64 [n]; < 0 reads as zeros).
+
+    The bytes of a page and head_dim give its tokens, but not the other way round: 64 tokens of 64 channels are as many
+    bytes as 32 of 128.  With page_size a cache made for another head_dim or page size is refused; without it one of as
+    many bytes is taken for what head_dim says.
+    """
     if dtype not in _HEAD_TYPES:
         raise ValueError("dtype must be bf16 or fp16")
-    P, Hkv, page_size = _pages(pages, head_dim)
+    P, Hkv, page_size = _pages(pages, head_dim, page_size)
     dev = _device(pages, slots, flags)
     n = slots.numel()
     k = pages.new_empty((n, Hkv, head_dim), dtype=dtype)
@@ -281,17 +286,19 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
 
 
 def cached_attention(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
-                     scale: float | None = None, window: int = 0, flags: torch.Tensor | None = None) -> torch.Tensor:
+                     scale: float | None = None, window: int = 0, flags: torch.Tensor | None = None,
+                     page_size: int | None = None) -> torch.Tensor:
     """Attention of one new token per sequence over its cached tokens: out [B][heads][d].
 
     q [B][heads][d] bf16 or fp16; block_table int32 [B][max_pages]; lens int32 [B], the cached tokens of each sequence
-    (the new one among them).  scale and window as in prompt_attention; an empty sequence gives a row of zeros.
+    (the new one among them).  scale and window as in prompt_attention, page_size as in kv_read; an empty sequence gives a
+    row of zeros.
     """
     dt = q.dtype
     if dt not in _HEAD_TYPES:
         raise ValueError("q must be bf16 or fp16")
     B, H, d, qs = _heads(q, dt, "q must be [B][heads][d], a token's heads contiguous")
-    P, Hkv, n = _pages(pages, d)
+    P, Hkv, n = _pages(pages, d, page_size)
     dev = _device(q, pages, block_table, lens, flags)
     if block_table.dtype is not torch.int32 or block_table.dim() != 2:
         raise ValueError("block_table must be int32 [B][max_pages]")

@@ -60,7 +60,7 @@ class AttentionLayer:
         qkv = int8_linear(resid, self.qkv, self.alpha_qkv, normalise=True, out_dtype=torch.bfloat16, flags=self.flags)
         q, k, v = qkv.view(-1, H + 2 * Hkv, d).split((H, Hkv, Hkv), 1)
         q, k = qk_norm_rope(q, k, positions, self.inv_freq, self.q_norm, self.k_norm, v=v, pages=self.pages, slots=slots,
-                            flags=self.flags)
+                            flags=self.flags, page_size=self.page_size)
         return q, k, v
 
     def _project(self, heads: torch.Tensor, resid: torch.Tensor) -> None:
@@ -76,7 +76,7 @@ class AttentionLayer:
         q, k, v = self._heads(resid, positions, slots)
         cu_k = cu
         if context is not None:
-            k, v = kv_read(self.pages, context[0], self.head_dim, dtype=q.dtype, flags=self.flags)
+            k, v = kv_read(self.pages, context[0], self.head_dim, dtype=q.dtype, flags=self.flags, page_size=self.page_size)
             cu_k = context[1]
         self._project(prompt_attention(q, k, v, cu, cu_k, max_len, window=self.window, flags=self.flags,
                                        out=torch.zeros_like(q)), resid)
@@ -86,7 +86,8 @@ class AttentionLayer:
                lens: torch.Tensor) -> torch.Tensor:
         """One new token per sequence (lens counts it); resid [B][d_model] is updated in place."""
         q, _, _ = self._heads(resid, positions, slots)
-        self._project(cached_attention(q, self.pages, block_table, lens, window=self.window, flags=self.flags), resid)
+        self._project(cached_attention(q, self.pages, block_table, lens, window=self.window, flags=self.flags,
+                                       page_size=self.page_size), resid)
         return resid
 
 

@@ -26,3 +26,21 @@ def test_stack_refuses_more_tokens_than_its_layers_take_before_it_starts():
     with pytest.raises(ValueError, match="9 tokens"):
         stack.prompt(resid, None, None, None, 9)
     assert first.calls == 0 and second.calls == 0
+
+
+# a page of 64 tokens of 64 channels has as many bytes as one of 32 tokens of 128 channels
+@pytest.mark.parametrize("made,other", [((64, 64), (128, 32)), ((64, 32), (128, 16)), ((128, 32), (64, 64)), ((128, 16), (64, 32))])
+def test_a_cache_of_another_head_dim_is_refused(made, other):
+    (d, n), (d2, n2) = made, other
+    pages = tw.kv_pages(2, 1, d, n, device="cpu")
+    assert pages.shape == tw.kv_pages(2, 1, d2, n2, device="cpu").shape
+    x, i64, i32 = torch.zeros(1, 1, d2, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int64), torch.zeros(1, dtype=torch.int32)
+    for call in (lambda h, **kw: tw.kv_read(pages, i64, h.shape[2], **kw),
+                 lambda h, **kw: tw.qk_norm_rope(h, h, i64, torch.zeros(0, dtype=torch.float64), v=h, pages=pages, slots=i64, **kw),
+                 lambda h, **kw: tw.cached_attention(h, pages, i32[None], i32, **kw)):
+        with pytest.raises(ValueError, match="do not fit this head_dim and page_size"):
+            call(x, page_size=n)
+        with pytest.raises(ValueError, match="CUDA device"):        # (past that check: the bytes alone fit)
+            call(x)
+        with pytest.raises(ValueError, match="CUDA device"):
+            call(torch.zeros(1, 1, d, dtype=torch.bfloat16), page_size=n)
