@@ -7,7 +7,9 @@
 // the row maximum only when a score passes it by 2^8: until then P stays below
 // 256, the sums stay exact in the same way, and O need not be rescaled.  P is
 // rounded to the inputs' type (the tensor cores' operand); l sums it before the
-// rounding.
+// rounding.  For fp16 heads P carries a factor of 2^7 (at most 2^15 then, fp16
+// ends at 2^16), which cancels in O / l: fp16's smallest step, 2^-24, is 2^-31 of
+// the reference so, and many weights far below the largest keep their share.
 //
 // Rows.  A tile is 128 rows = floor(128/G) query tokens x the G query heads of
 // one key/value head, so that grouped heads share every K and V tile (one 3-D
@@ -52,6 +54,8 @@ bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 // launch's 384 x 168 registers are shared out as 2 x 128 x 216 + 128 x 72
 constexpr int kThreads = 384;
 constexpr int kKeys = 128;   // keys of a tile
+template <typename T>
+constexpr float kLift = __is_same(T, __half) ? 7.0f : 0.0f;   // P carries a factor of 2^kLift
 
 template <int D>
 struct PromptSmem {
@@ -643,7 +647,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                         }
                     }
                 }
-                const float minus = m == -INFINITY ? 0.0f : -m;
+                const float minus = m == -INFINITY ? 0.0f : kLift<T> - m;
                 const uint64_t scale_2 = pair(scale2, scale2), minus_2 = pair(minus, minus);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -741,7 +745,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     }
                 }
             }
-            if (valid && a.lse) a.lse[row] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            if (valid && a.lse) a.lse[row] = none ? -INFINITY : (m + (log2f(l) - kLift<T>)) * 0.6931471805599453f;
             tc_fence_before();   // O is read before the next item's first product writes it (ordered by P's barrier)
         }
         if (n > 0) t0 += n + 1;

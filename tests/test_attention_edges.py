@@ -111,3 +111,26 @@ def test_cached_batch_without_a_token(H, Hkv, d, n):
                 junk = torch.full((B, H, d), 7.0, dtype=BF16, device="cuda")   # (its memory is the next output's)
                 del junk
                 assert torch.count_nonzero(tw.cached_attention(q, pages, table, lens) * 1.0).item() == 0
+
+
+@pytest.mark.parametrize("dt", [FP16, BF16])
+@pytest.mark.parametrize("n", [300, 4096, 65536])
+@pytest.mark.parametrize("gap", [14.3, 19.7, 23.4])
+@pytest.mark.parametrize("peak", [0, -1])
+def test_prompt_weights_far_below_the_largest(dt, n, gap, peak):
+    """One key 2^gap above all others, with a value of zero: the output is the others' share.  A weight is off by half a step
+    of its type, relative; of fp16 at least by half of the smallest step, 2^-25, where the largest weight is 2^7 or more:
+    2^-32 of the sum for each of n keys, times the values (1 here)."""
+    d, H = 64, 2
+    q, k, v = torch.zeros(3, H, d, device="cuda"), torch.zeros(n, 1, d, device="cuda"), torch.ones(n, 1, d, device="cuda")
+    q[..., 0] = 1
+    q[:, 1, 0] = 0.5
+    at = n - 3 if peak < 0 else 0                     # (the last of the keys that all three queries see)
+    k[at, 0, 0], v[at] = gap * math.log(2), 0
+    q, k, v = q.to(dt), k.to(dt), v.to(dt)
+    cu = lambda m: torch.tensor([0, m], dtype=torch.int32, device="cuda")  # noqa: E731
+    out, lse = tw.prompt_attention(q, k, v, cu(3), cu(n), 3, scale=1.0, return_lse=True)
+    want, bound, wlse = ref.prompt(q, k, v, [3], [n], 1.0, 0)
+    tol = ref.EPS[dt] * (1 + 2.0 ** -6) * (want.abs() + bound) + 2.0 ** -13 * bound + n * 2.0 ** -32
+    assert ((out.double() - want).abs() <= tol).all()
+    assert ((lse.double() - wlse).abs() <= 2.0 ** -13 + 2.0 ** -22 * wlse.abs()).all()
