@@ -7,17 +7,19 @@
 // cached side as the 16-row operand, so that 8 heads fill an instruction.  A
 // running maximum and sum per head make one pass over the cache enough.
 //
-// The 4-bit codes c go into the matrix instructions as fp16 integers, exactly:
-// (w & 0x000f000f) | 0x64006400 is the pair (1024 + c, 1024 + c'), and with
-// 0x00f000f0 it is 1024 + 16 c, whose partner q is divided by 16.  The constant
-// part, 1024 sum q (64 sum q), enters as the accumulator's start value.  With
-// scale s and minimum m of a token's group of 32 channels,
-//   q.k = sum_groups s_g (q_g . c_g) + m_g sum(q_g)
-// in 32 bits: the scores carry no rounding of the dequantised keys.  q is
-// brought to [1, 2) by a power of two per head first (exact), so that fp16
+// The 4-bit key codes c go into the matrix instructions as fp16 numbers, exactly:
+// w & 0x000f000f is the pair (c, c') in units of fp16's smallest step, 2^-24, and
+// with 0x00f000f0 it is 16 c, whose partner q is divided by 16.  With scale s and
+// minimum m of a token's group of 32 channels,
+//   q.k = 2^24 sum_groups s_g (q_g . c_g 2^-24) + sum_groups m_g sum(q_g)
+// in 32 bits: the scores carry no rounding of the dequantised keys and no constant
+// that cancels.  (As 1024 + c, with 1024 sum q taken off again, the partial sums
+// were a hundred times the result and their last bits showed in peaked rows.)  q
+// is brought to [1, 2) by a power of two per head first (exact), so that fp16
 // holds it whatever its size.  Values are dequantised to fp16 (one rounding,
-// 2^-12) and p, scaled by 2^4, is rounded to fp16 (bf16 outputs) or split in
-// two fp16 terms (fp16 outputs, where one rounding of p would show).
+// 2^-11; 1024 + c less 1024 is exact there) and p, scaled by 2^4, is rounded to
+// fp16 (bf16 outputs) or split in two fp16 terms (fp16 outputs, where one rounding
+// of p would show).
 //
 // Work split.  All (sequence, key/value head) segments are laid end to end in
 // units of 64 tokens and every CTA takes an equal share of the line, so that a
@@ -70,13 +72,12 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// the same with every row of the accumulator starting at (c0, c1)
-__device__ __forceinline__ void mma16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                           uint32_t b1, float c0, float c1)
+// the same with an accumulator of zeros
+__device__ __forceinline__ void mma16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t v)
 {
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
             // ---- queries: B fragments, their sums, and the softmax scale of this lane's two heads
             uint32_t qf[NT][G][4];
             uint32_t qs[NT][2];
-            float qb[NT][G][2], sc[NT][2];
+            float sc[NT][2];
 #pragma unroll
             for (int j = 0; j < NT; j++) {
                 const int h = j * 8 + g;
@@ -331,19 +332,16 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
                     unpack8<T>(raw[i], x);
 #pragma unroll
                     for (int m = 0; m < 8; m++) x[m] = x[m] * down * ((m & 1) ? 0.0625f : 1.0f);
-                    float sum = 0.0f, bias = 0.0f;
+                    float sum = 0.0f;
 #pragma unroll
                     for (int m = 0; m < 4; m++) {
                         const __half2 v = __floats2half2_rn(x[m], x[m + 4]);
                         qf[j][i][m] = as_u32(v);
                         const float2 f = __half22float2(v);
-                        bias += f.x + f.y;
                         sum += (m & 1) ? 16.0f * (f.x + f.y) : f.x + f.y;
                     }
                     sum += __shfl_xor_sync(FULL, sum, 1);
                     sum += __shfl_xor_sync(FULL, sum, 2);
-                    bias += __shfl_xor_sync(FULL, bias, 1);
-                    bias += __shfl_xor_sync(FULL, bias, 2);
                     if (i == t) {   // rows 2t+1 (the minima of group t) in two fp16 terms, 22 bits
                         const __half hi = __float2half_rn(sum);
                         const __half2 h2 = __halves2half2(__float2half_rn(0.0f), hi);
@@ -351,8 +349,6 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
                         qs[j][0] = as_u32(h2);
                         qs[j][1] = as_u32(l2);
                     }
-#pragma unroll
-                    for (int c = 0; c < 2; c++) qb[j][i][c] = -1024.0f * __shfl_sync(FULL, bias, (2 * t + c) * 4);
                 }
 #pragma unroll
                 for (int c = 0; c < 2; c++) sc[j][c] = __shfl_sync(FULL, mine_sc, (2 * t + c) * 4);
@@ -398,24 +394,29 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
                         // sum_groups m_g sum(q_g): the (scale, minimum) pairs themselves as the 16-row operand
                         const uint32_t mp0 = *(const uint32_t *)(base + P::k_pair(n, r0 + g, t % G));
                         const uint32_t mp1 = *(const uint32_t *)(base + P::k_pair(n, r0 + g + 8, t % G));
-#pragma unroll
-                        for (int j = 0; j < NT; j++) mma16_from(S[j][kb], mp0, mp1, mp0, mp1, qs[j][0], qs[j][1], 0.0f, 0.0f);
+                        float sum_c[NT][4];      // sum_groups s_g (q_g . c_g), in units of 2^-24
 #pragma unroll
                         for (int i = 0; i < G; i++) {
-                            const uint32_t a0 = lo_codes(w0[i]), a1 = lo_codes(w1[i]), a2 = hi_codes(w0[i]), a3 = hi_codes(w1[i]);
                             const uint32_t x0 = w0[i] >> 8, x1 = w1[i] >> 8;
-                            const uint32_t c0 = lo_codes(x0), c1 = lo_codes(x1), c2 = hi_codes(x0), c3 = hi_codes(x1);
+                            const uint32_t lo = 0x000f000fu, hi = 0x00f000f0u;
                             const float s0 = __low2float(as_h2(pr0[i])), s1 = __low2float(as_h2(pr1[i]));
 #pragma unroll
                             for (int j = 0; j < NT; j++) {
                                 float c[4];
-                                mma16_from(c, a0, a1, a2, a3, qf[j][i][0], qf[j][i][1], qb[j][i][0], qb[j][i][1]);
-                                mma16(c, c0, c1, c2, c3, qf[j][i][2], qf[j][i][3]);
-                                S[j][kb][0] = fmaf(s0, c[0], S[j][kb][0]);
-                                S[j][kb][1] = fmaf(s0, c[1], S[j][kb][1]);
-                                S[j][kb][2] = fmaf(s1, c[2], S[j][kb][2]);
-                                S[j][kb][3] = fmaf(s1, c[3], S[j][kb][3]);
+                                mma16_zero(c, w0[i] & lo, w1[i] & lo, w0[i] & hi, w1[i] & hi, qf[j][i][0], qf[j][i][1]);
+                                mma16(c, x0 & lo, x1 & lo, x0 & hi, x1 & hi, qf[j][i][2], qf[j][i][3]);
+#pragma unroll
+                                for (int e = 0; e < 4; e++) {
+                                    const float se = e < 2 ? s0 : s1;
+                                    sum_c[j][e] = i == 0 ? se * c[e] : fmaf(se, c[e], sum_c[j][e]);
+                                }
                             }
+                        }
+#pragma unroll
+                        for (int j = 0; j < NT; j++) {
+                            mma16_zero(S[j][kb], mp0, mp1, mp0, mp1, qs[j][0], qs[j][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; e++) S[j][kb][e] = fmaf(sum_c[j][e], 16777216.0f, S[j][kb][e]);
                         }
                         if (edge) {
                             const bool okp = (ok >> pg) & 1;

@@ -134,3 +134,35 @@ def test_prompt_weights_far_below_the_largest(dt, n, gap, peak):
     tol = ref.EPS[dt] * (1 + 2.0 ** -6) * (want.abs() + bound) + 2.0 ** -13 * bound + n * 2.0 ** -32
     assert ((out.double() - want).abs() <= tol).all()
     assert ((lse.double() - wlse).abs() <= 2.0 ** -13 + 2.0 ** -22 * wlse.abs()).all()
+
+
+@pytest.mark.parametrize("Hkv,d,n", [(1, 64, 16), (2, 128, 64), (1, 128, 32)])
+def test_cached_scores_keep_32_bits(Hkv, d, n):
+    """Queries of 1 in the even channels, 2^-4 or 2^-4 + 2^-14 in the odd ones; keys of codes 0..15 in steps of 1/8 (minimum
+    0), the even channels alike in all keys, the odd ones permuted: the scores, sums of at most 2^7 in steps of 2^-17,
+    have an exact value in 32 bits.  They are scaled far up, so that the weights show their last bits: scale |q.k| is
+    rounded twice on its way into the exponential (2^-24 of it each), and a weight counts twice (numerator and sum)."""
+    r, scale, H = gen(d + n), 8192.0, 8 * Hkv
+    lens = [2 + b % 4 for b in range(64)]
+    pages, table = tw.kv_pages(64, Hkv, d, n), torch.arange(64, dtype=torch.int32, device="cuda")[:, None]
+    codes = torch.arange(16, device="cuda") / 8
+    kv = []
+    for b, m in enumerate(lens):
+        odd = torch.stack([codes[torch.argsort(r(16))] for _ in range(m * Hkv * d // 32)]).view(m, Hkv, d // 2)
+        k = torch.stack([codes.repeat(d // 32).expand(m, Hkv, d // 2), odd], -1).flatten(-2)
+        slots = b * n + torch.arange(m, device="cuda")
+        ref.fill_pages(pages, n, k, r(m, Hkv, d), slots)
+        kv.append(ref.read_pages(pages, n, slots, d))
+        assert torch.equal(kv[b][0], k.double())
+    q = torch.ones(64, H, d)
+    q[..., 1::2] = 2.0 ** -4 + 2.0 ** -14 * torch.randint(0, 2, (64, H, d // 2), generator=torch.Generator().manual_seed(d))
+    q = q.cuda().to(FP16)
+    out = tw.cached_attention(q, pages, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), scale=scale)
+    for b, m in enumerate(lens):
+        k, v = kv[b]
+        for h in range(H):
+            want, bound, _ = ref.attend(q[b, h:h + 1], k[:, h // 8], v[:, h // 8], torch.ones(1, m, dtype=torch.bool, device="cuda"), scale)
+            top = (k[:, h // 8] @ q[b, h].double()).max() * scale
+            tol = ref.EPS[FP16] * (1 + 2.0 ** -6) * want.abs() + (2.0 ** -11 + 2.0 ** -13 + 4 * 2.0 ** -24 * top) * bound + 2.0 ** -24
+            err = (out[b, h].double() - want[0]).abs()
+            assert (err <= tol[0]).all(), (b, h, (err / tol[0]).max().item())
