@@ -12,7 +12,8 @@ synchronises, and all may be captured into a CUDA graph.  A tensor of the wrong
 type, shape, stride or device raises ValueError, an error of the library
 MapleError.  What only the kernels can see (a page number outside the cache) is
 reported in `flags`, an int32 tensor of one element that the caller zeroes and
-reads (MAPLE_FLAG_* bits).  No gradients: these are serving operators.
+reads (MAPLE_FLAG_* bits).  No gradients: these are serving operators, and a call
+with a tensor that requires one is refused unless gradients are off.
 
 Cache: uint8 [num_pages][kv_heads][page bytes], made by kv_pages(); a token's
 slot is page * page_size + row.
@@ -87,13 +88,18 @@ def _size(n: int, what: str) -> int:
 
 
 def _device(first, *others) -> int:
-    """The CUDA device index that all tensors (None aside) are on."""
-    dev = first.get_device()
+    """The CUDA device index that all tensors (None aside) are on, none of which a gradient is asked for."""
+    dev, grad = first.get_device(), first.requires_grad
+    for t in others:
+        if t is not None:
+            if t.get_device() != dev:
+                raise ValueError("all tensors must be on one device")
+            if t.requires_grad:
+                grad = True
+    if grad and torch.is_grad_enabled():
+        raise ValueError("no gradients are computed here: detach the tensors that require one, or call under torch.no_grad()")
     if dev < 0:
         raise ValueError("the tensors must be on a CUDA device")
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("all tensors must be on one device")
     return dev
 
 

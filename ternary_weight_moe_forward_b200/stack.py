@@ -38,7 +38,7 @@ class AttentionLayer:
         def dev(name, dtype, shape):
             if weights.get(name) is None:
                 return None
-            t = torch.as_tensor(weights[name]).to(device=device, dtype=dtype).contiguous()
+            t = torch.as_tensor(weights[name]).detach().to(device=device, dtype=dtype).contiguous()
             if tuple(t.shape) != shape:
                 raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
             return t

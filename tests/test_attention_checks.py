@@ -44,3 +44,34 @@ def test_a_cache_of_another_head_dim_is_refused(made, other):
             call(x)
         with pytest.raises(ValueError, match="CUDA device"):
             call(torch.zeros(1, 1, d, dtype=torch.bfloat16), page_size=n)
+
+
+@pytest.mark.parametrize("which", ["x", "alpha", "bias", "resid", "out"])
+def test_linear_refuses_to_lose_a_gradient(which):
+    t = dict(x=torch.zeros(2, 64, dtype=torch.bfloat16), alpha=torch.zeros(8), bias=torch.zeros(8), resid=torch.zeros(2, 8),
+             out=torch.zeros(2, 8))
+    w = torch.zeros(8, 64, dtype=torch.int8)
+    t[which].requires_grad_()
+    with pytest.raises(ValueError, match="no gradients"):
+        tw.int8_linear(t.pop("x"), w, t.pop("alpha"), **t)
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_attention_refuses_to_lose_a_gradient(which):
+    h = [torch.zeros(2, 1, 64, dtype=torch.bfloat16) for _ in range(4)]
+    h[which].requires_grad_()
+    q, k, v, out = h
+    i64, i32, f64 = torch.zeros(2, dtype=torch.int64), torch.zeros(2, dtype=torch.int32), torch.zeros(0, dtype=torch.float64)
+    pages = tw.kv_pages(1, 1, 64, 16, device="cpu")
+    with pytest.raises(ValueError, match="no gradients"):
+        tw.prompt_attention(q, k, v, i32, i32, 2, out=out)
+    if which < 3:
+        with pytest.raises(ValueError, match="no gradients"):
+            tw.qk_norm_rope(q, k, i64, f64, v=v, pages=pages, slots=i64)
+    if which == 0:
+        with pytest.raises(ValueError, match="no gradients"):
+            tw.cached_attention(q, pages, i32[:, None], i32)
+        with pytest.raises(ValueError, match="no gradients"):
+            tw.qk_norm_rope(k, k, i64, f64, torch.ones(64, requires_grad=True))
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):        # (past that check)
+            tw.cached_attention(q, pages, i32[:, None], i32)

@@ -166,3 +166,21 @@ def test_cached_scores_keep_32_bits(Hkv, d, n):
             tol = ref.EPS[FP16] * (1 + 2.0 ** -6) * want.abs() + (2.0 ** -11 + 2.0 ** -13 + 4 * 2.0 ** -24 * top) * bound + 2.0 ** -24
             err = (out[b, h].double() - want[0]).abs()
             assert (err <= tol[0]).all(), (b, h, (err / tol[0]).max().item())
+
+
+def test_parameters_serve_without_gradients():
+    """Tensors that require a gradient: refused, unless gradients are off; a layer takes its weights without."""
+    x, w = torch.ones(2, 256, dtype=BF16, device="cuda"), torch.ones(8, 256, dtype=torch.int8, device="cuda")
+    al = torch.nn.Parameter(torch.ones(8, device="cuda"))
+    with pytest.raises(ValueError, match="no gradients"):
+        tw.int8_linear(x, w, al)
+    for off in (torch.no_grad, torch.inference_mode):
+        with off():
+            assert (tw.int8_linear(x, w, al) == 256).all()
+    from ternary_weight_moe_forward_b200 import synth
+    weights = synth.attention_weights(256, 4, 2, 64, 5)
+    weights["q_norm"] = torch.nn.Parameter(torch.from_numpy(weights["q_norm"]))
+    attn = tw.AttentionLayer(256, 4, 2, 64, weights, 4, page_size=16)
+    i = torch.arange(4, device="cuda")
+    r = attn.prompt(gen(1)(4, 256), i, i, torch.tensor([0, 4], dtype=torch.int32, device="cuda"), 4)
+    assert r.isfinite().all() and not r.requires_grad
