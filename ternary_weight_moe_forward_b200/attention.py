@@ -131,6 +131,15 @@ def _heads(t, dtype, what: str):
     return n, h, d, (step if n > 1 else h * d)
 
 
+def _overlap(out, t) -> bool:
+    """Whether the contiguous tensor `out` reaches into the memory from the first to the last element of t."""
+    if t is None or not out.numel() or not t.numel():
+        return False
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    a, b = out.data_ptr(), t.data_ptr()
+    return a < b + (last + 1) * t.element_size() and b < a + out.numel() * out.element_size()
+
+
 def kv_pages(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, device="cuda") -> torch.Tensor:
     """A zeroed cache of `num_pages` pages of `page_size` tokens (16, 32 or 64) with head_dim 64 or 128."""
     b = _size(_lib().maple_attn_page_bytes(head_dim, page_size), "maple_attn_page_bytes")
@@ -154,8 +163,9 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias
     """y = (q_x weight^T) * (s_x alpha) (+ bias) (+ resid), q_x and s_x the int8 absmax codes and scales of x's rows.
 
     x bf16 [T][K] (rows may be strided), or the fp32 residual stream with `normalise` (its RMS-normed rows, rounded to
-    bf16, are quantised).  weight int8 [N][K], alpha fp32 [N], bias fp32 [N], resid fp32 [T][N] (may be `out`).  x must
-    not overlap `out`.  A row of x with a NaN or an infinity gives a row of NaN.
+    bf16, are quantised).  weight int8 [N][K], alpha fp32 [N], bias fp32 [N], resid fp32 [T][N].  `out`, where given, sets
+    the output's type; it may be resid and overlaps nothing else that is read.  A row of x with a NaN or an infinity gives a
+    row of NaN.
     """
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("x must be [T][K] and weight [N][K]")
@@ -177,8 +187,12 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias
         out = x.new_empty((T, N), dtype=out_dtype)
     elif out.shape != (T, N) or not out.is_contiguous():
         raise ValueError("out must be contiguous [T][N]")
-    elif T and out.data_ptr() == x.data_ptr():
-        raise ValueError("x must not be out")
+    elif _overlap(out, x):
+        raise ValueError("x must not be out or overlap it")
+    elif resid is not None and _overlap(out, resid) and (out.dtype is not torch.float32 or out.data_ptr() != resid.data_ptr()):
+        raise ValueError("resid must be out or not overlap it")
+    elif _overlap(out, weight) or _overlap(out, alpha) or _overlap(out, bias):
+        raise ValueError("out must not overlap weight, alpha or bias")
     ydt = _OUT_TYPES.get(out.dtype)
     if ydt is None:
         raise ValueError("the output must be bf16 or fp32")
@@ -280,8 +294,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
         out = torch.empty_like(q, memory_format=_CONTIGUOUS)
     elif out.dtype is not dt or out.shape != (Tq, H, d) or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's type and shape")
-    elif Tq and out.data_ptr() in (q.data_ptr(), k.data_ptr(), v.data_ptr()):
-        raise ValueError("out must not be q, k or v")
+    elif _overlap(out, q) or _overlap(out, k) or _overlap(out, v):
+        raise ValueError("out must not be q, k or v or overlap them")
     lse = q.new_empty((Tq, H), dtype=torch.float32) if return_lse else None
     _call("prompt", _PROMPT.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),

@@ -75,3 +75,18 @@ def test_attention_refuses_to_lose_a_gradient(which):
             tw.qk_norm_rope(k, k, i64, f64, torch.ones(64, requires_grad=True))
         with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):        # (past that check)
             tw.cached_attention(q, pages, i32[:, None], i32)
+
+
+
+
+def test_the_memory_of_out():
+    from ternary_weight_moe_forward_b200.attention import _overlap
+    buf = torch.zeros(100)
+    at = lambda a, n, *s: buf[a:a + n].view(*s)  # noqa: E731
+    out = at(20, 12, 3, 4)
+    for t, hit in ((None, False), (at(0, 20, 20), False), (at(0, 21, 21), True), (at(31, 1, 1), True), (at(32, 8, 8), False),
+                   (buf.as_strided((2, 4), (50, 1), 0), True), (buf.as_strided((2, 4), (16, 1), 0), False),
+                   (buf.as_strided((2, 4), (17, 1), 0), True), (buf.as_strided((3, 4), (0, 1), 16), False),
+                   (buf.as_strided((3, 5), (0, 1), 16), True), (buf[25:25], False), (out.view(torch.int32), True)):
+        assert _overlap(out, t) is hit
+    assert not _overlap(buf[20:20], buf)

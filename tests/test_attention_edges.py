@@ -184,3 +184,28 @@ def test_parameters_serve_without_gradients():
     i = torch.arange(4, device="cuda")
     r = attn.prompt(gen(1)(4, 256), i, i, torch.tensor([0, 4], dtype=torch.int32, device="cuda"), 4)
     assert r.isfinite().all() and not r.requires_grad
+
+
+def test_out_that_reaches_into_what_is_read():
+    """An output anywhere in memory that the call reads is refused; the residual itself and neighbours are not."""
+    mem = torch.ones(40, 256, device="cuda")
+    w, al = torch.ones(256, 256, dtype=torch.int8, device="cuda"), torch.ones(256, device="cuda")
+    x = mem[:8]
+    with pytest.raises(ValueError, match="x must not be out"):
+        tw.int8_linear(x, w, al, normalise=True, out=mem[7:15])
+    with pytest.raises(ValueError, match="resid must be out"):
+        tw.int8_linear(x, w, al, normalise=True, resid=mem[8:16], out=mem[15:23])
+    with pytest.raises(ValueError, match="resid must be out"):
+        tw.int8_linear(x, w, al, normalise=True, resid=mem[8:16], out=mem[8:12].view(BF16).view(8, 256))
+    with pytest.raises(ValueError, match="weight, alpha or bias"):
+        tw.int8_linear(x, w, mem[20], normalise=True, out=mem[16:24])
+    want = tw.int8_linear(x, w, al, normalise=True, resid=mem[8:16])
+    assert torch.equal(tw.int8_linear(x, w, al, normalise=True, resid=mem[8:16], out=mem[8:16]), want)
+    assert torch.equal(tw.int8_linear(x, w, al, normalise=True, resid=mem[24:32], out=mem[16:24]), want)
+    mem = torch.ones(60, 2, 64, dtype=FP16, device="cuda")
+    q, k, v = mem[:10], mem[10:20], mem[20:30]
+    c = torch.tensor([0, 10], dtype=torch.int32, device="cuda")
+    for a in (1, 9, 11, 19, 29):
+        with pytest.raises(ValueError, match="out must not be"):
+            tw.prompt_attention(q, k, v, c, c, 10, out=mem[a:a + 10])
+    assert (tw.prompt_attention(q, k, v, c, c, 10, out=mem[30:40]) == 1).all()
