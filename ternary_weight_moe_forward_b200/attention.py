@@ -67,6 +67,13 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
+def _pack(form: struct.Struct, *fields) -> bytes:
+    try:
+        return form.pack(*fields)
+    except (struct.error, OverflowError) as e:      # (sizes beyond 32 bits, a scale beyond fp32, what is no number)
+        raise ValueError(f"an argument does not fit its field: {e}") from None
+
+
 def _call(name: str, args: bytes, dev: int) -> None:
     """Launch on the device's current stream, with that device current."""
     if _fn is None:
@@ -198,7 +205,7 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias
         raise ValueError("the output must be bf16 or fp32")
     n = _size((_fn or _lib()).maple_attn_linear_workspace(T, K, N, 1 if normalise else 0), "maple_attn_linear")
     ws = x.new_empty(n, dtype=torch.uint8) if n else None
-    _call("linear", _LINEAR.pack(
+    _call("linear", _pack(_LINEAR,
         x.data_ptr(), weight.data_ptr(), _vector(alpha, torch.float32, N, "alpha must be fp32 [N]"),
         _vector(bias, torch.float32, N, "bias must be fp32 [N]"), 0 if resid is None else resid.data_ptr(), out.data_ptr(),
         0 if ws is None else ws.data_ptr(), n, _flags(flags), step if T > 1 else K, T, K, N, ydt, 1 if normalise else 0), dev)
@@ -237,7 +244,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_
     qo = torch.empty_like(q, memory_format=_CONTIGUOUS)
     ko = torch.empty_like(k, memory_format=_CONTIGUOUS)
     rot = inv_freq.shape[0]
-    _call("qk_norm_rope", _ROPE.pack(
+    _call("qk_norm_rope", _pack(_ROPE,
         q.data_ptr(), k.data_ptr(), vp, qo.data_ptr(), ko.data_ptr(),
         _vector(q_weight, torch.float32, d, "q_weight must be fp32 [head_dim]"),
         _vector(k_weight, torch.float32, d, "k_weight must be fp32 [head_dim]"),
@@ -263,7 +270,7 @@ def kv_read(pages: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: torc
     n = slots.numel()
     k = pages.new_empty((n, Hkv, head_dim), dtype=dtype)
     v = torch.empty_like(k)
-    _call("kv_read", _READ.pack(pages.data_ptr(), _vector(slots, torch.int64, n, "slots must be int64 [n]"), k.data_ptr(),
+    _call("kv_read", _pack(_READ, pages.data_ptr(), _vector(slots, torch.int64, n, "slots must be int64 [n]"), k.data_ptr(),
                                 v.data_ptr(), _flags(flags), n, P, Hkv, head_dim, page_size, _HEAD_TYPES[dtype]), dev)
     return k, v
 
@@ -297,7 +304,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     elif _overlap(out, q) or _overlap(out, k) or _overlap(out, v):
         raise ValueError("out must not be q, k or v or overlap them")
     lse = q.new_empty((Tq, H), dtype=torch.float32) if return_lse else None
-    _call("prompt", _PROMPT.pack(
+    _call("prompt", _pack(_PROMPT,
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
         _vector(cu_q, torch.int32, B + 1, "cu_q must be int32 [B+1]"), _vector(cu_k, torch.int32, B + 1, "cu_k must be int32 [B+1]"),
         _flags(flags), qs, ks, vs, Tq, Tk, B, max_q, H, Hkv, d, window, _HEAD_TYPES[dt], d ** -0.5 if scale is None else scale),
@@ -329,7 +336,7 @@ def cached_attention(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Te
     out = torch.empty_like(q, memory_format=_CONTIGUOUS)
     w = _size((_fn or _lib()).maple_attn_cached_workspace(B, mp, H, Hkv, d, n, window), "maple_attn_cached")
     ws = q.new_empty(w, dtype=torch.uint8) if w else None
-    _call("cached", _CACHED.pack(
+    _call("cached", _pack(_CACHED,
         q.data_ptr(), out.data_ptr(), pages.data_ptr(), block_table.data_ptr(), _vector(lens, torch.int32, B, "lens must be int32 [B]"),
         0 if ws is None else ws.data_ptr(), w, _flags(flags), qs, step if B > 1 else mp, P, B, mp, H, Hkv, d, n, window,
         _HEAD_TYPES[dt], d ** -0.5 if scale is None else scale), dev)

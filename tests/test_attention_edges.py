@@ -209,3 +209,24 @@ def test_out_that_reaches_into_what_is_read():
         with pytest.raises(ValueError, match="out must not be"):
             tw.prompt_attention(q, k, v, c, c, 10, out=mem[a:a + 10])
     assert (tw.prompt_attention(q, k, v, c, c, 10, out=mem[30:40]) == 1).all()
+
+
+def test_numbers_that_do_not_fit():
+    """Numbers beyond the fields of the C arguments are refused like other wrong arguments."""
+    h = torch.ones(2, 1, 64, dtype=FP16, device="cuda")
+    c, pages = torch.tensor([0, 2], dtype=torch.int32, device="cuda"), tw.kv_pages(1, 1, 64, 16)
+    pos, f = torch.arange(2, device="cuda"), torch.zeros(0, dtype=torch.float64, device="cuda")
+    for call in (lambda: tw.prompt_attention(h, h, h, c, c, 2, window=1 << 31), lambda: tw.prompt_attention(h, h, h, c, c, 1 << 40),
+                 lambda: tw.prompt_attention(h, h, h, c, c, 2, scale=1e39), lambda: tw.prompt_attention(h, h, h, c, c, 2.0),
+                 lambda: tw.cached_attention(h, pages, c[:, None], c, window=1 << 32),
+                 lambda: tw.cached_attention(h, pages, c[:, None], c, scale=-1e300),
+                 lambda: tw.qk_norm_rope(h, h, pos, f, eps=1e200)):
+        with pytest.raises(ValueError, match="does not fit"):
+            call()
+    for scale in (math.inf, math.nan):
+        with pytest.raises(tw.MapleError):
+            tw.prompt_attention(h, h, h, c, c, 2, scale=scale)
+    # the widest window is no window
+    assert torch.equal(tw.prompt_attention(h, h, h, c, c, 2, window=(1 << 31) - 1), tw.prompt_attention(h, h, h, c, c, 2))
+    assert torch.equal(tw.cached_attention(h, pages, c[:, None] * 0, c, window=(1 << 31) - 1),
+                       tw.cached_attention(h, pages, c[:, None] * 0, c))
