@@ -37,7 +37,9 @@ class AttentionLayer:
                  page_size: int = 64, rotary_dim: int | None = None, theta: float = 10000.0, device="cuda"):
         def dev(name, dtype, shape):
             if weights.get(name) is None:
-                return None
+                if name in ("q_norm", "k_norm"):
+                    return None
+                raise ValueError(f"{name} is missing")
             t = torch.as_tensor(weights[name]).detach().to(device=device, dtype=dtype).contiguous()
             if tuple(t.shape) != shape:
                 raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")

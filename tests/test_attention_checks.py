@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import ternary_weight_moe_forward_b200 as tw
+from ternary_weight_moe_forward_b200 import synth
 
 
 class Recorder:
@@ -90,3 +91,15 @@ def test_the_memory_of_out():
                    (buf.as_strided((3, 5), (0, 1), 16), True), (buf[25:25], False), (out.view(torch.int32), True)):
         assert _overlap(out, t) is hit
     assert not _overlap(buf[20:20], buf)
+
+
+@pytest.mark.parametrize("name", ["qkv", "alpha_qkv", "out", "alpha_out", "q_norm", "k_norm"])
+def test_a_layer_needs_its_weights(name):
+    weights = synth.attention_weights(256, 4, 2, 64, 5)
+    weights[name] = None
+    if name.endswith("norm"):
+        assert getattr(tw.AttentionLayer(256, 4, 2, 64, weights, 1, device="cpu"), name) is None
+        return
+    for w in (weights, {k: v for k, v in weights.items() if k != name}):
+        with pytest.raises(ValueError, match=f"{name} is missing"):
+            tw.AttentionLayer(256, 4, 2, 64, w, 1, device="cpu")
