@@ -156,6 +156,8 @@ int maple_attn_kv_read(const maple_attn_read_args *args, maple_stream_t stream);
  * to no sequence are left as they were; out and lse overlap nothing that the
  * call reads.  What stands in masked keys and values
  * (infinities, NaN) does not reach the output.
+ * Limits: at most 64 query heads per key/value head and 1024 in all, 65535
+ * sequences, 2^30 rows of queries and of keys.
  * max_q bounds every lq from above (a sequence with more query rows raises
  * MAPLE_FLAG_BAD_INDEX and loses the rows beyond max_q); offsets that fall or
  * reach beyond Tq or Tk are cut to them and raise MAPLE_FLAG_BAD_INDEX.
@@ -181,6 +183,7 @@ int maple_attn_prompt(const maple_attn_prompt_args *args, maple_stream_t stream)
  * window as above.  lens[b] <= 0 gives a row of zeros; lens[b] is cut to
  * max_pages*page_size (MAPLE_FLAG_BAD_INDEX).  A page number outside the cache
  * is skipped as if its positions were masked (MAPLE_FLAG_BAD_INDEX).
+ * Limits: 1024 query heads, 65535 sequences, max_pages * page_size <= 2^30.
  */
 typedef struct {
     const void *q;                  /* [B][heads][d] */

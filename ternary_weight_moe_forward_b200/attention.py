@@ -67,17 +67,14 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _pack(form: struct.Struct, *fields) -> bytes:
-    try:
-        return form.pack(*fields)
-    except (struct.error, OverflowError) as e:      # (sizes beyond 32 bits, a scale beyond fp32, what is no number)
-        raise ValueError(f"an argument does not fit its field: {e}") from None
-
-
-def _call(name: str, args: bytes, dev: int) -> None:
-    """Launch on the device's current stream, with that device current."""
+def _call(name: str, form: struct.Struct, fields: tuple, dev: int) -> None:
+    """Launch with the argument struct's fields on the device's current stream, with that device current."""
     if _fn is None:
         _lib()
+    try:
+        args = form.pack(*fields)
+    except (struct.error, OverflowError) as e:      # (sizes beyond 32 bits, a scale beyond fp32, what is no number)
+        raise ValueError(f"an argument does not fit its field: {e}") from None
     stream = _raw_stream(dev)
     if dev == _current_device():
         rc = _calls[name](args, stream)
@@ -95,19 +92,20 @@ def _size(n: int, what: str) -> int:
 
 
 def _device(first, *others) -> int:
-    """The CUDA device index that all tensors (None aside) are on, none of which a gradient is asked for."""
-    dev, grad = first.get_device(), first.requires_grad
-    for t in others:
-        if t is not None:
-            if t.get_device() != dev:
-                raise ValueError("all tensors must be on one device")
-            if t.requires_grad:
-                grad = True
-    if grad and torch.is_grad_enabled():
-        raise ValueError("no gradients are computed here: detach the tensors that require one, or call under torch.no_grad()")
+    """The CUDA device index that all tensors (None aside) are on."""
+    dev = first.get_device()
     if dev < 0:
         raise ValueError("the tensors must be on a CUDA device")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on one device")
     return dev
+
+
+def _refuse_gradient() -> None:
+    """For a call with a tensor that requires a gradient."""
+    if torch.is_grad_enabled():
+        raise ValueError("no gradients are computed here: detach the tensors that require one, or call under torch.no_grad()")
 
 
 def _flags(t) -> int:
@@ -181,6 +179,9 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias
     if K != Kw:
         raise ValueError("x must be [T][K] and weight [N][K]")
     step, one = x.stride()
+    if (x.requires_grad or alpha.requires_grad or (bias is not None and bias.requires_grad) or
+            (resid is not None and resid.requires_grad) or (out is not None and out.requires_grad)):
+        _refuse_gradient()
     dev = _device(x, weight, alpha, bias, resid, out, flags)
     if x.dtype is not (torch.float32 if normalise else torch.bfloat16):
         raise ValueError("x must be bf16, or fp32 with normalise")
@@ -205,7 +206,7 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias
         raise ValueError("the output must be bf16 or fp32")
     n = _size((_fn or _lib()).maple_attn_linear_workspace(T, K, N, 1 if normalise else 0), "maple_attn_linear")
     ws = x.new_empty(n, dtype=torch.uint8) if n else None
-    _call("linear", _pack(_LINEAR,
+    _call("linear", _LINEAR, (
         x.data_ptr(), weight.data_ptr(), _vector(alpha, torch.float32, N, "alpha must be fp32 [N]"),
         _vector(bias, torch.float32, N, "bias must be fp32 [N]"), 0 if resid is None else resid.data_ptr(), out.data_ptr(),
         0 if ws is None else ws.data_ptr(), n, _flags(flags), step if T > 1 else K, T, K, N, ydt, 1 if normalise else 0), dev)
@@ -240,11 +241,14 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_
         vp, pp = v.data_ptr(), pages.data_ptr()
     elif v is not None or slots is not None:
         raise ValueError("pages, v and slots go together")
+    if (q.requires_grad or k.requires_grad or (v is not None and v.requires_grad) or inv_freq.requires_grad or
+            (q_weight is not None and q_weight.requires_grad) or (k_weight is not None and k_weight.requires_grad)):
+        _refuse_gradient()
     dev = _device(q, k, positions, inv_freq, q_weight, k_weight, v, pages, slots, flags)
     qo = torch.empty_like(q, memory_format=_CONTIGUOUS)
     ko = torch.empty_like(k, memory_format=_CONTIGUOUS)
     rot = inv_freq.shape[0]
-    _call("qk_norm_rope", _pack(_ROPE,
+    _call("qk_norm_rope", _ROPE, (
         q.data_ptr(), k.data_ptr(), vp, qo.data_ptr(), ko.data_ptr(),
         _vector(q_weight, torch.float32, d, "q_weight must be fp32 [head_dim]"),
         _vector(k_weight, torch.float32, d, "k_weight must be fp32 [head_dim]"),
@@ -270,8 +274,8 @@ def kv_read(pages: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: torc
     n = slots.numel()
     k = pages.new_empty((n, Hkv, head_dim), dtype=dtype)
     v = torch.empty_like(k)
-    _call("kv_read", _pack(_READ, pages.data_ptr(), _vector(slots, torch.int64, n, "slots must be int64 [n]"), k.data_ptr(),
-                                v.data_ptr(), _flags(flags), n, P, Hkv, head_dim, page_size, _HEAD_TYPES[dtype]), dev)
+    _call("kv_read", _READ, (pages.data_ptr(), _vector(slots, torch.int64, n, "slots must be int64 [n]"), k.data_ptr(),
+                              v.data_ptr(), _flags(flags), n, P, Hkv, head_dim, page_size, _HEAD_TYPES[dtype]), dev)
     return k, v
 
 
@@ -293,6 +297,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     vs = _heads(v, dt, "v must be [Tk][kv_heads][d] of q's type, a token's heads contiguous")[3]
     if k.shape != v.shape or dk != d:
         raise ValueError("k and v must have one shape and q's head_dim")
+    if q.requires_grad or k.requires_grad or v.requires_grad or (out is not None and out.requires_grad):
+        _refuse_gradient()
     dev = _device(q, k, v, cu_q, cu_k, out, flags)
     B = cu_q.numel() - 1
     if B < 0:
@@ -304,7 +310,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     elif _overlap(out, q) or _overlap(out, k) or _overlap(out, v):
         raise ValueError("out must not be q, k or v or overlap them")
     lse = q.new_empty((Tq, H), dtype=torch.float32) if return_lse else None
-    _call("prompt", _pack(_PROMPT,
+    _call("prompt", _PROMPT, (
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
         _vector(cu_q, torch.int32, B + 1, "cu_q must be int32 [B+1]"), _vector(cu_k, torch.int32, B + 1, "cu_k must be int32 [B+1]"),
         _flags(flags), qs, ks, vs, Tq, Tk, B, max_q, H, Hkv, d, window, _HEAD_TYPES[dt], d ** -0.5 if scale is None else scale),
@@ -326,6 +332,8 @@ def cached_attention(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Te
         raise ValueError("q must be bf16 or fp16")
     B, H, d, qs = _heads(q, dt, "q must be [B][heads][d], a token's heads contiguous")
     P, Hkv, n = _pages(pages, d, page_size)
+    if q.requires_grad:
+        _refuse_gradient()
     dev = _device(q, pages, block_table, lens, flags)
     if block_table.dtype is not torch.int32 or block_table.dim() != 2:
         raise ValueError("block_table must be int32 [B][max_pages]")
@@ -336,7 +344,7 @@ def cached_attention(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Te
     out = torch.empty_like(q, memory_format=_CONTIGUOUS)
     w = _size((_fn or _lib()).maple_attn_cached_workspace(B, mp, H, Hkv, d, n, window), "maple_attn_cached")
     ws = q.new_empty(w, dtype=torch.uint8) if w else None
-    _call("cached", _pack(_CACHED,
+    _call("cached", _CACHED, (
         q.data_ptr(), out.data_ptr(), pages.data_ptr(), block_table.data_ptr(), _vector(lens, torch.int32, B, "lens must be int32 [B]"),
         0 if ws is None else ws.data_ptr(), w, _flags(flags), qs, step if B > 1 else mp, P, B, mp, H, Hkv, d, n, window,
         _HEAD_TYPES[dt], d ** -0.5 if scale is None else scale), dev)

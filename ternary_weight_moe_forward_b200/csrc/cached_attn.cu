@@ -46,7 +46,7 @@ namespace {
 
 constexpr int kStages = 2, kTile = 64;   // tiles of a ring, tokens of a tile
 constexpr int kCtas = 148;          // CTAs that share the line of all segments (one per SM)
-constexpr int kSegCost = 12;        // tiles that a segment's own start and end are worth (64 ragged sequences: 4 108 us, 12 98, 24 99)
+constexpr int kSegCost = 12;        // tiles that a segment's own start and end are worth (64 ragged sequences: 4 104.7 us, 12 94.2, 24 95.6)
 constexpr int kWholeTiles = 16;     // segments of at most so many tiles: one CTA each, no combine
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -113,12 +113,13 @@ struct Span {
     }
 };
 
-// How many CTAs share a line of `total` weight: each has 8 tiles at least
+// How many CTAs share a line of `total` weight (tiles, and kSegCost for each segment): as few as leave each at most 8
+// units, up to all of them.  A CTA whose share lies in segments' starts alone has no tile.
 __device__ __forceinline__ int sharers(int64_t total) { return (int)min((int64_t)kCtas, (total + 7) / 8); }
 
-// One warp per ring.  (Two warps to a tile, 16 in all with 128 registers each,
-// took 108 us where one took 96: what a tile costs beside its tokens was paid
-// twice.)  16 heads leave room for 8 warps' accumulators.
+// One warp per ring.  (In an earlier version two warps to a tile, 16 in all with
+// 128 registers each, took 108 us where one took 96: what a tile costs beside its
+// tokens was paid twice.)  16 heads leave room for 8 warps' accumulators.
 template <int D, int NT>
 struct CachedSmem {
     static constexpr int kWarps = NT == 1 ? 10 : 8, kHalf = (kWarps + 1) / 2;
@@ -676,8 +677,11 @@ __global__ void __launch_bounds__(CachedSmem<D, NT>::kWarps * 32, 1) cached_kern
 // (sequence, column, head), its 8 warps taking every eighth partial result and
 // summed in order, so that all loads are in flight at once (a loop over the
 // partial results by one thread per output cost 40 us for 75 of them).  A warp's
-// first ten partial results are loaded before their factors are known: one
-// sequence of 131071 tokens takes 22.6 us in all instead of 26.5.
+// first kEarly partial results are loaded before their factors are known: one
+// sequence of 131071 tokens took 22.6 us in all instead of 26.5.  Ten for each of 8
+// warps hold the 74 or 75 that one sequence over two key/value heads leaves (six:
+// 22.9 to 23.7 us against 22.5); more, up to 148 with one key/value head, go through
+// the loop behind them.  They cost a ragged batch, which has few, 0.3 of 94.2 us.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(256, 4) combine_kernel(const CachedK p)
 {

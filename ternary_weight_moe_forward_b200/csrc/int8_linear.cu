@@ -685,10 +685,11 @@ int rows_smem(int64_t T, int K)
     return 8 * NT * row_pitch(K) + 2 * kRowWarps * NT * 512;
 }
 // With the norm every block reads the fp32 rows three times, which pays up to 16384
-// values: the two launches of the other path take 13.2 us for one row of 2048 into
-// 2560 columns and this kernel 9.2, 14.0 and 12.3 for 8 rows of 2048, 21.8 and 17.5
-// for 4 of 4096; but 14.4 and 21.4 for 16 of 2048, 37.1 and 39.0 for 4 of 8192 (16 of
-// 1024 are the one measured loss inside the rule: 10.6 and 12.2).
+// values: into 2560 columns the two launches of the other path take 13.6 us for one
+// row of 2048 and this kernel 9.4, 14.2 and 12.4 for 8 rows; into 4096 columns 21.7
+// and 17.5 for 4 rows of 4096.  Above it loses: 14.4 and 21.4 for 16 rows of 2048,
+// 37.1 and 39.0 for 4 of 8192.  (16 rows of 1024 are the one measured loss inside the
+// rule: 10.5 and 12.2.)
 bool rows_path(int64_t T, int K, bool normalise)
 {
     return T <= kRowTokens && rows_smem(T, K) <= kRowCodes && (!normalise || T * K <= 16384);
