@@ -179,7 +179,7 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, alpha: torch.Tensor, bias
     if K != Kw:
         raise ValueError("x must be [T][K] and weight [N][K]")
     step, one = x.stride()
-    if (x.requires_grad or alpha.requires_grad or (bias is not None and bias.requires_grad) or
+    if (x.requires_grad or (alpha is not None and alpha.requires_grad) or (bias is not None and bias.requires_grad) or
             (resid is not None and resid.requires_grad) or (out is not None and out.requires_grad)):
         _refuse_gradient()
     dev = _device(x, weight, alpha, bias, resid, out, flags)

@@ -230,3 +230,9 @@ def test_numbers_that_do_not_fit():
     assert torch.equal(tw.prompt_attention(h, h, h, c, c, 2, window=(1 << 31) - 1), tw.prompt_attention(h, h, h, c, c, 2))
     assert torch.equal(tw.cached_attention(h, pages, c[:, None] * 0, c, window=(1 << 31) - 1),
                        tw.cached_attention(h, pages, c[:, None] * 0, c))
+
+
+def test_linear_without_scales_is_refused():
+    x, w = torch.ones(2, 64, dtype=BF16, device="cuda"), torch.ones(8, 64, dtype=torch.int8, device="cuda")
+    with pytest.raises(tw.MapleError):
+        tw.int8_linear(x, w, None)
